@@ -469,6 +469,139 @@ BI_API bi_status bi_moe_forward_noalloc(const bi_bf16 *x, const int32_t *ids,
                                         bi_stream_t stream);
 
 /* ======================================================================
+ * Dense gated feed-forward block (a shared, always active expert): forward,
+ * its backward pass, and its 4-bit serving form.
+ * ======================================================================
+ *
+ * With W13 = [Wg; Wu] (gate rows first, as the routed experts' W13):
+ *   forward   [g u] = x W13^T,  act = silu(g) u,  out = act W2^T (+ addend)
+ *   backward  dact = dout W2,  s = 1 / (1 + exp(-g)),
+ *             dg = dact u s (1 + g (1 - s)),  du = dact g s,
+ *             dx = [dg du] W13,  dW13 = [dg du]^T x,  dW2 = dout^T act
+ *   (the gradient of addend is dout itself).
+ * All sums are fp32.  Rounded to bf16: act (the operand of the down product
+ * and of dW2), dg and du (the operands of dx and dW13), and each result once;
+ * g and u stay fp32 from forward to backward.
+ * Batch invariance: a row of out and of dx has the same bits whatever M is and
+ * whatever other rows share the call (the reduction recipe is fixed by the
+ * reduction length alone).  dW13 and dW2 sum over the tokens in a fixed
+ * order: the same call gives the same bits.
+ * Requirements: H and I multiples of 16 and at most 2^20, M <= 2^30 (else
+ * BI_ERR_UNSUPPORTED); pointers 16-byte aligned, the row strides ld* (in
+ * elements) multiples of 8 and at least H.
+ *
+ * bi_ffn_workspace_bytes -- bytes that cover the workspace of bi_ffn_forward
+ * (M * I bf16) and of bi_ffn_backward (M * 2I bf16); 0 for invalid sizes.
+ */
+BI_API size_t bi_ffn_workspace_bytes(int64_t M, int64_t H, int64_t I);
+
+/*
+ * bi_ffn_forward -- out for inference, one token or many.
+ *   x [M,H] bf16, row stride ldx;  w13 [2I,H] bf16;  w2 [H,I] bf16
+ *   addend [M,H] bf16, row stride ld_addend, or NULL: added in fp32 before the
+ *     one rounding of out (the routed experts' output; out may be addend)
+ *   out [M,H] bf16, row stride ldo, written
+ *   workspace: 256-byte aligned, at least M * I * 2 bytes, contents need not
+ *     be initialised.
+ */
+BI_API bi_status bi_ffn_forward(const bi_bf16 *x, int64_t ldx, const bi_bf16 *w13,
+                                const bi_bf16 *w2, const bi_bf16 *addend, int64_t ld_addend,
+                                bi_bf16 *out, int64_t ldo, int64_t M, int64_t H, int64_t I,
+                                void *workspace, size_t workspace_bytes, bi_stream_t stream);
+
+/*
+ * bi_ffn_forward_train -- bi_ffn_forward (same bits of out) that also keeps
+ * what bi_ffn_backward reads:
+ *   gu  [M,2I] fp32, written: row m holds g, then u
+ *   act [M,I] bf16, written
+ */
+BI_API bi_status bi_ffn_forward_train(const bi_bf16 *x, int64_t ldx, const bi_bf16 *w13,
+                                      const bi_bf16 *w2, const bi_bf16 *addend,
+                                      int64_t ld_addend, bi_bf16 *out, int64_t ldo, float *gu,
+                                      bi_bf16 *act, int64_t M, int64_t H, int64_t I,
+                                      bi_stream_t stream);
+
+/*
+ * bi_ffn_backward -- gradients from dout [M,H] bf16 (row stride lddo).
+ *   x, w13, w2: the forward's;  gu, act: kept by bi_ffn_forward_train
+ *   dx   [M,H] bf16, row stride lddx, written, or NULL (not computed)
+ *   dw13 [2I,H], dw2 [H,I], or NULL each (not computed)
+ *   grad_mode: 0 dw13 and dw2 are bf16, written; 1 fp32, written; 2 fp32,
+ *     the gradient is added to what they hold (micro-batches)
+ *   workspace: 256-byte aligned, at least M * 2I * 2 bytes (dg and du), not
+ *     needed when both dx and dw13 are NULL.
+ * M == 0: dw13 and dw2 are set to zero (grad_mode 2: left as they are).
+ */
+BI_API bi_status bi_ffn_backward(const bi_bf16 *dout, int64_t lddo, const bi_bf16 *x, int64_t ldx,
+                                 const bi_bf16 *w13, const bi_bf16 *w2, const float *gu,
+                                 const bi_bf16 *act, bi_bf16 *dx, int64_t lddx, void *dw13,
+                                 void *dw2, int32_t grad_mode, int64_t M, int64_t H, int64_t I,
+                                 void *workspace, size_t workspace_bytes, bi_stream_t stream);
+
+/* ---- microscaled 4-bit floating point -----------------------------------
+ *
+ * The Open Compute Project's MXFP4: 32 consecutive values of a row share a
+ * scale, a power of two (E8M0 byte b: 2^(b - 127); 255: NaN); each value is a
+ * 4-bit code (E2M1: 0, .5, 1, 1.5, 2, 3, 4, 6 and a sign in bit 3) times it.
+ *   codes  [R, K/2] uint8 row-major: element 2j in the low half of byte j
+ *   scales: tiles of 128 rows x 4 scales (128 x 128 values), 512 bytes each,
+ *     in row-tile major order [ceil(R/128)][ceil(K/128)]; the scale of row r,
+ *     block b (values 32b..32b+31) is byte (r % 32) * 16 + (r / 32 % 4) * 4 +
+ *     b % 4 of tile (r / 128, b / 4).  Bytes of rows past R and blocks past
+ *     K/32 are padding: bi_mx4_quantize writes 0, and a caller that builds the
+ *     tiles itself must not leave 255 in the blocks past K/32.
+ * K % 32 == 0, K <= 2^20, R <= 2^30 (else BI_ERR_UNSUPPORTED); codes and scales
+ * 16-byte aligned.
+ *
+ * bi_mx4_scale_bytes -- bytes of the scale tiles of [R, K] (0 for invalid sizes).
+ */
+BI_API size_t bi_mx4_scale_bytes(int64_t R, int64_t K);
+
+/*
+ * bi_mx4_quantize -- codes and scales of x [R,K] (bf16, or fp32 when x_f32 is
+ * not 0; 16-byte aligned, row stride ldx a multiple of 8).  The scale of a
+ * block whose largest magnitude is m 2^e, 1 <= m < 2, is 2^(e-2), at least
+ * 2^-127; its values are divided by it (exact) and rounded to the nearest code,
+ * ties to the even code, magnitudes above 6 to 6; the sign of zero is kept.  A
+ * block that holds a NaN or an infinity gets scale 255 and zero codes.
+ */
+BI_API bi_status bi_mx4_quantize(const void *x, int32_t x_f32, int64_t ldx, uint8_t *q,
+                                 uint8_t *scales, int64_t R, int64_t K, bi_stream_t stream);
+
+/*
+ * bi_mx4_dequantize -- y [R,K] (bf16, or fp32 when y_f32 is not 0; 16-byte
+ * aligned, row stride ldy a multiple of 8), written: code times scale, exact
+ * (in bf16 too), NaN for a NaN scale.
+ */
+BI_API bi_status bi_mx4_dequantize(const uint8_t *q, const uint8_t *scales, void *y,
+                                   int32_t y_f32, int64_t ldy, int64_t R, int64_t K,
+                                   bi_stream_t stream);
+
+/*
+ * bi_mx4_gemm -- y [M,N] bf16 = X W^T (+ addend), X [M,K] and W [N,K] in the
+ * 4-bit form above (any M, any N <= 2^22).  Sums are fp32, one rounding.  A
+ * row's bits do not depend on M or on other rows.  A NaN scale makes the rows
+ * (columns) of y that use it NaN.
+ *   addend [M,N] bf16, row stride ld_addend, or NULL; y may be addend
+ *   y row stride ldy (elements, any ldy >= N), written.
+ */
+BI_API bi_status bi_mx4_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq,
+                             const uint8_t *ws, const bi_bf16 *addend, int64_t ld_addend,
+                             bi_bf16 *y, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                             bi_stream_t stream);
+
+/*
+ * bi_mx4_gate_up -- act [M,I] bf16 = silu(X Wg^T) * (X Wu^T), both projections,
+ * the activation and the product in one kernel.  The weight's 2I rows are
+ * interleaved before they are quantised: 16 gate rows, the up rows of the same
+ * 16 features, and so on (row 32 j + i: gate row 16 j + i for i < 16, up row
+ * 16 j + i - 16 for i >= 16).  I % 16 == 0.
+ */
+BI_API bi_status bi_mx4_gate_up(const uint8_t *xq, const uint8_t *xs, const uint8_t *w13q,
+                                const uint8_t *w13s, bi_bf16 *act, int64_t ld_act, int64_t M,
+                                int64_t I, int64_t K, bi_stream_t stream);
+
+/* ======================================================================
  * TEST AND MEASUREMENT HOOKS.  Not part of the hot path and not needed to
  * use it: the test-suite and the benchmark call these to force schedules
  * (and show the bits do not depend on them), to run the negative control,

@@ -1,13 +1,14 @@
 // api.cu -- the extern "C" entry points of libbimoe.so: argument checks,
 // workspace layout, TMA descriptor encoding, and the device error word.
-// All arithmetic happens in the kernels of router.cu, topk.cu, moe_route.cu
-// and moe_gemm.cu.
+// All arithmetic happens in the kernels of router.cu, topk.cu, moe_route.cu,
+// moe_gemm.cu, ffn.cu and mx4.cu.
 #include <cstdarg>
 #include <cstdio>
 #include <atomic>
 #include <mutex>
 
 #include "bimoe_internal.cuh"
+#include "ffn_internal.cuh"
 
 namespace bimoe {
 
@@ -747,3 +748,184 @@ BI_API bi_status bi_moe_gemm_variant(int32_t variant, int32_t *previous) {
   if (previous) *previous = old;
   return BI_OK;
 }
+
+// -------------------------------------- dense gated feed-forward block --
+static bi_status check_ffn_dims(int64_t M, int64_t H, int64_t I) {
+  BI_REQUIRE(M >= 0 && H > 0 && I > 0, BI_ERR_INVALID_ARG, "negative or zero size (M=%lld H=%lld I=%lld)",
+             (long long)M, (long long)H, (long long)I);
+  BI_REQUIRE(H % 16 == 0 && I % 16 == 0, BI_ERR_UNSUPPORTED,
+             "unsupported feed-forward shape (needs H %% 16 == 0, I %% 16 == 0): H=%lld I=%lld", (long long)H,
+             (long long)I);
+  BI_REQUIRE(M <= (int64_t(1) << 30) && H <= (int64_t(1) << 20) && I <= (int64_t(1) << 20), BI_ERR_UNSUPPORTED,
+             "feed-forward sizes exceed the index range (M=%lld H=%lld I=%lld)", (long long)M, (long long)H,
+             (long long)I);
+  return BI_OK;
+}
+
+// A token matrix [M, cols] with row stride ld: 16-byte rows, as the copies want them.
+static bi_status check_rows(const char *name, const void *p, int64_t ld, int64_t cols) {
+  BI_REQUIRE(p, BI_ERR_INVALID_ARG, "%s is NULL", name);
+  BI_REQUIRE(aligned(p, 16), BI_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  BI_REQUIRE(ld >= cols && ld % 8 == 0 && ld <= (int64_t(1) << 30), BI_ERR_INVALID_ARG,
+             "row stride of %s: %lld (needs a multiple of 8, at least %lld)", name, (long long)ld, (long long)cols);
+  return BI_OK;
+}
+
+static Mat mat(const bi_bf16 *p, int64_t ld) { return Mat{reinterpret_cast<const __nv_bfloat16 *>(p), ld}; }
+static const __nv_bfloat16 *cbf(const void *p) { return static_cast<const __nv_bfloat16 *>(p); }
+static __nv_bfloat16 *mbf(void *p) { return static_cast<__nv_bfloat16 *>(p); }
+
+#define BI_TRY(call)                       \
+  do {                                     \
+    const bi_status st_ = (call);          \
+    if (st_ != BI_OK) return st_;          \
+  } while (0)
+
+extern "C" {
+
+BI_API size_t bi_ffn_workspace_bytes(int64_t M, int64_t H, int64_t I) {
+  if (check_ffn_dims(M, H, I) != BI_OK) return 0;
+  return std::max<size_t>(256, align256(static_cast<size_t>(M) * 2 * I * sizeof(bi_bf16)));
+}
+
+static bi_status ffn_forward_impl(const bi_bf16 *x, int64_t ldx, const bi_bf16 *w13, const bi_bf16 *w2,
+                                  const bi_bf16 *addend, int64_t ld_addend, bi_bf16 *out, int64_t ldo, float *gu,
+                                  void *act, int64_t M, int64_t H, int64_t I, bi_stream_t stream) {
+  BI_TRY(check_rows("x", x, ldx, H));
+  BI_TRY(check_rows("out", out, ldo, H));
+  if (addend) BI_TRY(check_rows("addend", addend, ld_addend, H));
+  BI_REQUIRE(w13 && w2, BI_ERR_INVALID_ARG, "null pointer");
+  BI_REQUIRE(aligned(w13, 16) && aligned(w2, 16), BI_ERR_INVALID_ARG, "w13 and w2 must be 16-byte aligned");
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  BI_TRY(launch_ffn_gate_up(mat(x, ldx), cbf(w13), mbf(act), gu, M, H, I, s));
+  return launch_ffn_down(cbf(act), cbf(w2), mat(addend, ld_addend), mbf(out), ldo, M, H, I, s);
+}
+
+BI_API bi_status bi_ffn_forward(const bi_bf16 *x, int64_t ldx, const bi_bf16 *w13, const bi_bf16 *w2,
+                                const bi_bf16 *addend, int64_t ld_addend, bi_bf16 *out, int64_t ldo, int64_t M,
+                                int64_t H, int64_t I, void *workspace, size_t workspace_bytes, bi_stream_t stream) {
+  BI_TRY(check_ffn_dims(M, H, I));
+  if (M == 0) return BI_OK;
+  const size_t need = static_cast<size_t>(M) * I * sizeof(bi_bf16);
+  BI_REQUIRE(workspace && aligned(workspace, 256), BI_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  BI_REQUIRE(workspace_bytes >= need, BI_ERR_WORKSPACE, "workspace %zu < %zu bytes", workspace_bytes, need);
+  return ffn_forward_impl(x, ldx, w13, w2, addend, ld_addend, out, ldo, nullptr, workspace, M, H, I, stream);
+}
+
+BI_API bi_status bi_ffn_forward_train(const bi_bf16 *x, int64_t ldx, const bi_bf16 *w13, const bi_bf16 *w2,
+                                      const bi_bf16 *addend, int64_t ld_addend, bi_bf16 *out, int64_t ldo, float *gu,
+                                      bi_bf16 *act, int64_t M, int64_t H, int64_t I, bi_stream_t stream) {
+  BI_TRY(check_ffn_dims(M, H, I));
+  if (M == 0) return BI_OK;
+  BI_REQUIRE(gu && act, BI_ERR_INVALID_ARG, "null pointer");
+  BI_REQUIRE(aligned(gu, 16) && aligned(act, 16), BI_ERR_INVALID_ARG, "gu and act must be 16-byte aligned");
+  return ffn_forward_impl(x, ldx, w13, w2, addend, ld_addend, out, ldo, gu, act, M, H, I, stream);
+}
+
+BI_API bi_status bi_ffn_backward(const bi_bf16 *dout, int64_t lddo, const bi_bf16 *x, int64_t ldx, const bi_bf16 *w13,
+                                 const bi_bf16 *w2, const float *gu, const bi_bf16 *act, bi_bf16 *dx, int64_t lddx,
+                                 void *dw13, void *dw2, int32_t grad_mode, int64_t M, int64_t H, int64_t I,
+                                 void *workspace, size_t workspace_bytes, bi_stream_t stream) {
+  BI_TRY(check_ffn_dims(M, H, I));
+  BI_REQUIRE(grad_mode >= 0 && grad_mode <= 2, BI_ERR_INVALID_ARG, "grad_mode %d not in {0, 1, 2}", grad_mode);
+  BI_REQUIRE(aligned(dw13, 16) && aligned(dw2, 16), BI_ERR_INVALID_ARG, "dw13 and dw2 must be 16-byte aligned");
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    // no tokens: the weight gradients are zero (or stay as they are, when added to)
+    const size_t item = grad_mode == kGradBf16 ? 2 : 4;
+    cudaError_t e = cudaSuccess;
+    if (grad_mode != kGradF32Accumulate && dw13)
+      e = cudaMemsetAsync(dw13, 0, static_cast<size_t>(2 * I) * H * item, s);
+    if (e == cudaSuccess && grad_mode != kGradF32Accumulate && dw2)
+      e = cudaMemsetAsync(dw2, 0, static_cast<size_t>(I) * H * item, s);
+    BI_REQUIRE(e == cudaSuccess, BI_ERR_CUDA, "cudaMemsetAsync: %s", cudaGetErrorString(e));
+    return BI_OK;
+  }
+  if (!dx && !dw13 && !dw2) return BI_OK;
+  BI_TRY(check_rows("dout", dout, lddo, H));
+  if (dx) BI_TRY(check_rows("dx", dx, lddx, H));
+  if (dw13) BI_TRY(check_rows("x", x, ldx, H));
+  BI_REQUIRE(w2 && gu && (w13 || !dx) && (act || !dw2), BI_ERR_INVALID_ARG, "null pointer");
+  BI_REQUIRE(aligned(w13, 16) && aligned(w2, 16) && aligned(gu, 16) && aligned(act, 16), BI_ERR_INVALID_ARG,
+             "w13, w2, gu and act must be 16-byte aligned");
+  __nv_bfloat16 *dgu = mbf(workspace);
+  if (dx || dw13) {
+    const size_t need = static_cast<size_t>(M) * 2 * I * sizeof(bi_bf16);
+    BI_REQUIRE(workspace && aligned(workspace, 256), BI_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    BI_REQUIRE(workspace_bytes >= need, BI_ERR_WORKSPACE, "workspace %zu < %zu bytes", workspace_bytes, need);
+    BI_TRY(launch_ffn_dact(mat(dout, lddo), cbf(w2), gu, dgu, M, H, I, s));
+  }
+  if (dw2) BI_TRY(launch_ffn_wgrad(mat(dout, lddo), mat(act, I), dw2, grad_mode, M, H, I, s));
+  if (dx) BI_TRY(launch_ffn_dx(dgu, cbf(w13), mbf(dx), lddx, M, H, I, s));
+  if (dw13) BI_TRY(launch_ffn_wgrad(Mat{dgu, 2 * I}, mat(x, ldx), dw13, grad_mode, M, 2 * I, H, s));
+  return BI_OK;
+}
+
+// ------------------------------------- microscaled 4-bit floating point --
+static bi_status check_mx4_dims(const char *rows, int64_t R, int64_t K) {
+  BI_REQUIRE(R >= 0 && K > 0, BI_ERR_INVALID_ARG, "bad sizes %s=%lld K=%lld", rows, (long long)R, (long long)K);
+  BI_REQUIRE(K % kMxBlock == 0, BI_ERR_UNSUPPORTED, "K must be a multiple of 32 (K=%lld)", (long long)K);
+  BI_REQUIRE(R <= (int64_t(1) << 30) && K <= (int64_t(1) << 20), BI_ERR_UNSUPPORTED,
+             "sizes exceed the index range (%s=%lld K=%lld)", rows, (long long)R, (long long)K);
+  return BI_OK;
+}
+
+BI_API size_t bi_mx4_scale_bytes(int64_t R, int64_t K) {
+  if (check_mx4_dims("R", R, K) != BI_OK) return 0;
+  return static_cast<size_t>((R + kMxTileRows - 1) / kMxTileRows) * ((K + 127) / 128) * kMxTileBytes;
+}
+
+BI_API bi_status bi_mx4_quantize(const void *x, int32_t x_f32, int64_t ldx, uint8_t *q, uint8_t *scales, int64_t R,
+                                 int64_t K, bi_stream_t stream) {
+  BI_TRY(check_mx4_dims("R", R, K));
+  if (R == 0) return BI_OK;
+  BI_TRY(check_rows("x", x, ldx, K));
+  BI_REQUIRE(q && scales && aligned(q, 16) && aligned(scales, 16), BI_ERR_INVALID_ARG,
+             "q and scales must be 16-byte aligned");
+  return launch_mx4_quantize(x, x_f32 != 0, ldx, q, scales, R, K, reinterpret_cast<cudaStream_t>(stream));
+}
+
+BI_API bi_status bi_mx4_dequantize(const uint8_t *q, const uint8_t *scales, void *y, int32_t y_f32, int64_t ldy,
+                                   int64_t R, int64_t K, bi_stream_t stream) {
+  BI_TRY(check_mx4_dims("R", R, K));
+  if (R == 0) return BI_OK;
+  BI_TRY(check_rows("y", y, ldy, K));
+  BI_REQUIRE(q && scales && aligned(q, 16) && aligned(scales, 16), BI_ERR_INVALID_ARG,
+             "q and scales must be 16-byte aligned");
+  return launch_mx4_dequantize(q, scales, y, y_f32 != 0, ldy, R, K, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static bi_status mx4_product(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
+                             const bi_bf16 *addend, int64_t ld_addend, bi_bf16 *y, int64_t ldy, bool gated, int64_t M,
+                             int64_t N, int64_t K, bi_stream_t stream) {
+  BI_TRY(check_mx4_dims("M", M, K));
+  BI_REQUIRE(N > 0, BI_ERR_INVALID_ARG, "bad size N=%lld", (long long)N);
+  BI_REQUIRE(N <= (int64_t(1) << 22), BI_ERR_UNSUPPORTED, "N exceeds the index range (N=%lld)", (long long)N);
+  if (M == 0) return BI_OK;
+  BI_REQUIRE(xq && xs && wq && ws && y, BI_ERR_INVALID_ARG, "null pointer");
+  BI_REQUIRE(aligned(xq, 16) && aligned(xs, 16) && aligned(wq, 16) && aligned(ws, 16), BI_ERR_INVALID_ARG,
+             "codes and scales must be 16-byte aligned");
+  const int64_t cols = gated ? N / 2 : N;
+  BI_REQUIRE(ldy >= cols && ldy <= (int64_t(1) << 30), BI_ERR_INVALID_ARG, "row stride of y: %lld < %lld",
+             (long long)ldy, (long long)cols);
+  BI_REQUIRE(!addend || (ld_addend >= cols && ld_addend <= (int64_t(1) << 30)), BI_ERR_INVALID_ARG,
+             "row stride of addend: %lld < %lld", (long long)ld_addend, (long long)cols);
+  BI_REQUIRE(aligned(y, 2) && aligned(addend, 2), BI_ERR_INVALID_ARG, "y and addend must be 2-byte aligned");
+  return launch_mx4_gemm(xq, xs, wq, ws, mat(addend, ld_addend), mbf(y), ldy, gated, M, N, K,
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+BI_API bi_status bi_mx4_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws,
+                             const bi_bf16 *addend, int64_t ld_addend, bi_bf16 *y, int64_t ldy, int64_t M, int64_t N,
+                             int64_t K, bi_stream_t stream) {
+  return mx4_product(xq, xs, wq, ws, addend, ld_addend, y, ldy, false, M, N, K, stream);
+}
+
+BI_API bi_status bi_mx4_gate_up(const uint8_t *xq, const uint8_t *xs, const uint8_t *w13q, const uint8_t *w13s,
+                                bi_bf16 *act, int64_t ld_act, int64_t M, int64_t I, int64_t K, bi_stream_t stream) {
+  BI_REQUIRE(I > 0, BI_ERR_INVALID_ARG, "bad size I=%lld", (long long)I);
+  BI_REQUIRE(I % 16 == 0, BI_ERR_UNSUPPORTED, "I must be a multiple of 16 (I=%lld)", (long long)I);
+  return mx4_product(xq, xs, w13q, w13s, nullptr, 0, act, ld_act, true, M, 2 * I, K, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,46 @@
+// ffn_internal.cuh -- host-side interfaces of the dense gated feed-forward
+// block (ffn.cu) and of the microscaled 4-bit operators (mx4.cu), shared with
+// the entry points in api.cu.
+#pragma once
+
+#include "bimoe_internal.cuh"
+
+namespace bimoe {
+
+// A row-major bf16 matrix [rows, cols] with row stride ld (elements).
+struct Mat {
+  const __nv_bfloat16 *p;
+  int64_t ld;
+};
+
+enum GradMode { kGradBf16 = 0, kGradF32 = 1, kGradF32Accumulate = 2 };
+
+// act [M, I] = silu(x Wg^T) * (x Wu^T); gu [M, 2I] fp32 (may be null) keeps the two projections.
+bi_status launch_ffn_gate_up(Mat x, const __nv_bfloat16 *w13, __nv_bfloat16 *act, float *gu, int64_t M, int64_t H,
+                             int64_t I, cudaStream_t s);
+// out [M, H] = act W2^T (+ addend)
+bi_status launch_ffn_down(const __nv_bfloat16 *act, const __nv_bfloat16 *w2, Mat addend, __nv_bfloat16 *out,
+                          int64_t ldo, int64_t M, int64_t H, int64_t I, cudaStream_t s);
+// dgu [M, 2I] = the gradient of the two projections, from dact = dout W2
+bi_status launch_ffn_dact(Mat dout, const __nv_bfloat16 *w2, const float *gu, __nv_bfloat16 *dgu, int64_t M, int64_t H,
+                          int64_t I, cudaStream_t s);
+// dx [M, H] = dgu W13
+bi_status launch_ffn_dx(const __nv_bfloat16 *dgu, const __nv_bfloat16 *w13, __nv_bfloat16 *dx, int64_t lddx, int64_t M,
+                        int64_t H, int64_t I, cudaStream_t s);
+// dw [rows, cols] = a^T b over M tokens, a [M, rows], b [M, cols]
+bi_status launch_ffn_wgrad(Mat a, Mat b, void *dw, int grad_mode, int64_t M, int64_t rows, int64_t cols,
+                           cudaStream_t s);
+
+constexpr int kMxBlock = 32;       // values that share a scale
+constexpr int kMxTileRows = 128;   // a scale tile: 128 rows x 4 scales, 512 bytes
+constexpr int kMxTileScales = 4;
+constexpr int kMxTileBytes = 512;
+
+bi_status launch_mx4_quantize(const void *x, bool f32, int64_t ldx, uint8_t *q, uint8_t *scales, int64_t R, int64_t K,
+                              cudaStream_t s);
+bi_status launch_mx4_dequantize(const uint8_t *q, const uint8_t *scales, void *y, bool f32, int64_t ldy, int64_t R,
+                                int64_t K, cudaStream_t s);
+bi_status launch_mx4_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws, Mat addend,
+                          __nv_bfloat16 *y, int64_t ldy, bool gated, int64_t M, int64_t N, int64_t K, cudaStream_t s);
+
+}  // namespace bimoe
