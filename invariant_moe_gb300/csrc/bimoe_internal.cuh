@@ -52,6 +52,10 @@ bool make_tma_2d_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_
 // same features (I rows further), and so on for four groups: 64 features'
 // interleaved rows in one copy, 128-byte swizzled like the 2-D map's.
 bool make_tma_inter_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t I, uint64_t K);
+// Encode a 2-D bf16 TMA map over [rows, cols] with row stride ld (elements) and
+// a [box_rows, 64]-element box, 128-byte swizzle.
+bool make_tma_2d_bf16_ld(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld,
+                         uint32_t box_rows);
 bool make_tma_2d_f32(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                      uint32_t box_rows);
 void set_error(const char *fmt, ...);
@@ -501,6 +505,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+// 32 lanes x 16 consecutive fp32 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -519,6 +533,24 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
   d |= static_cast<uint64_t>(2) << 61;            // 128-byte swizzle
   return d;
 }
+
+// Descriptor of an MN-major operand tile written by TMA with 128-byte swizzle:
+// slabs of 64 M/N elements (128 B) x `slab_k` rows of k, each slab slab_k *
+// 128 bytes (leading byte offset, from one slab of 64 M/N elements to the
+// next), its 8-row groups of k 1024 B apart (stride byte offset).  Stepping K
+// by 16 adds two groups, 2048 B, to the start address.
+__device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t slab_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(slab_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+// Instruction-descriptor bits that mark A / B as MN-major (kind::f16).
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
 
 // Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator, bf16 A
 // and B, both K-major, shape M x N.

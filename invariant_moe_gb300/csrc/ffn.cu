@@ -1,134 +1,515 @@
 // ffn.cu -- the dense gated feed-forward block (a shared expert), forward and
-// backward.
+// backward, on 5th-generation tensor cores.
 //
 //   forward   [g u] = x W13^T,  act = silu(g) u,  out = act W2^T (+ addend)
 //   backward  dact = dout W2,  s = 1 / (1 + exp(-g)),
 //             dg = dact u s (1 + g (1 - s)),  du = dact g s,
 //             dx = [dg du] W13,  dW13 = [dg du]^T x,  dW2 = dout^T act
 //
-// One tile kernel over fp32 FMAs: 64 x 64 outputs per CTA, 4 x 4 per thread,
-// operands read through their two strides, every output one chain of fused
-// multiply-adds over increasing k.  The chain depends on the reduction length
-// alone, so a token's row has the same bits whatever M is.
+// Six products, one kernel template.  The left operand A (weights; for the
+// weight gradients the token matrix whose columns become dW's rows) gives the
+// 256 rows of a tile, the right operand B (tokens; for the weight gradients the
+// other matrix' columns) its up to 256 columns.
+//   * Operands come as they lie in memory.  Where the reduction index is the
+//     contiguous one they are K-major tiles, where it is the row index (W2 in
+//     dact, W13 in dx, all operands of the weight gradients) MN-major ones:
+//     nothing is transposed in memory.
+//   * CTA pairs (cta_group::2): each CTA stages its own 128 rows of A and half
+//     of B's, one thread of the even CTA issues M=256 MMAs over both.  A K step
+//     of 64 is 32 KB per SM, six of them in flight.
+//   * Recipe.  The reduction is cut into slices of 1024; a slice is one chain of
+//     K=16 MMAs in tensor memory and the slices are added in fp32 in increasing
+//     order, from +0, by the epilogue warps in registers while the next slice runs.  The
+//     recipe depends on the reduction length alone, so a token's row of out and
+//     dx has the same bits in every batch.  (The weight gradients reduce over
+//     the tokens: one slice.)
+//   * Eight epilogue warps, 32 rows x half of the columns each, keep the tile in
+//     registers, so tensor memory is free again before anything is stored.
+//     gate/up: each CTA holds 64 gate rows and the matching 64 up rows in
+//     16-row groups, so a lane and lane ^ 16 hold both projections of a feature.
+#include <mutex>
+
 #include "ffn_internal.cuh"
 
 namespace bimoe {
 
-constexpr int kT = 64;   // outputs per tile side
-constexpr int kTK = 16;  // reduction step
+constexpr int kFM = 128;                       // rows of A per CTA
+constexpr int kFK = 64;                        // reduction step of a stage
+constexpr int kFStages = 6;
+constexpr int kFABytes = kFM * kFK * 2;        // 16 KB
+constexpr int kFBBytes = 128 * kFK * 2;        // 16 KB: at most 128 rows of B per CTA
+constexpr int kFStageBytes = kFABytes + kFBBytes;
+constexpr int kFSlab = 64 * kFK * 2;           // an MN-major slab: 64 rows or columns x 64 k
+constexpr int kFAccCols = 256;
+constexpr int kFThreads = 320;                 // TMA, MMA, 8 epilogue warps
+constexpr int kFSmem = 1024 + kFStages * kFStageBytes + 256;
+constexpr int kSliceK = 1024;                  // reduction slice of the recipe
+static_assert(kFSmem <= 227 * 1024, "shared memory");
 
-struct Strided {
-  const __nv_bfloat16 *p;
-  int64_t s_row, s_k;
-};
+enum FfnEpi { kGateUp, kStore, kDact, kWgrad };
 
-enum Epi { kEpiGateUp, kEpiStore, kEpiDact, kEpiWgrad };
-
-struct FfnParams {
-  Strided a, b, b2;  // D[m, n] = sum_k a[m, k] b[n, k]; b2: the up rows (gate/up)
-  int64_t M, N, K;
+struct FfnGemm {
+  int rows, cols;       // valid rows (A side; features) and columns (B side; tokens) of the result
+  int m_tiles, n_tiles; // tiles of 256 rows (gate/up: 128 features) and n columns
+  int n;                // columns of a tile: the MMA's N, a multiple of 32
+  int nkb, slice_kb;    // K steps of 64, and how many make a slice
   void *out;
   int64_t ldo;
-  const __nv_bfloat16 *addend;
+  const __nv_bfloat16 *addend;  // kStore
   int64_t ld_add;
-  float *gu;
-  int mode;
+  float *gu;            // kGateUp: written (may be null); kDact: read
+  int mode;             // kWgrad: GradMode
+  int *err;
 };
 
-template <Epi EPI>
-__global__ void __launch_bounds__(256) ffn_tile_kernel(const FfnParams p) {
-  constexpr bool kTwo = EPI == kEpiGateUp;
-  __shared__ float as[kTK][kT + 1], bs[kTwo ? 2 : 1][kTK][kT + 1];
-  griddep_wait();
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kT, n0 = static_cast<int64_t>(blockIdx.y) * kT;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  float acc[kTwo ? 2 : 1][4][4] = {};
-  for (int64_t k0 = 0; k0 < p.K; k0 += kTK) {
-    for (int i = threadIdx.x; i < kT * kTK; i += 256) {
-      // consecutive threads along whichever index is contiguous in memory
-      const int ra = p.a.s_k == 1 ? i / kTK : i % kT, ka = p.a.s_k == 1 ? i % kTK : i / kT;
-      const int rb = p.b.s_k == 1 ? i / kTK : i % kT, kb = p.b.s_k == 1 ? i % kTK : i / kT;
-      const bool oka = m0 + ra < p.M && k0 + ka < p.K, okb = n0 + rb < p.N && k0 + kb < p.K;
-      as[ka][ra] = oka ? __bfloat162float(p.a.p[(m0 + ra) * p.a.s_row + (k0 + ka) * p.a.s_k]) : 0.0f;
-      bs[0][kb][rb] = okb ? __bfloat162float(p.b.p[(n0 + rb) * p.b.s_row + (k0 + kb) * p.b.s_k]) : 0.0f;
-      if (kTwo) bs[1][kb][rb] = okb ? __bfloat162float(p.b2.p[(n0 + rb) * p.b2.s_row + (k0 + kb) * p.b2.s_k]) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kTK; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[0][i][j] = fmaf(as[k][ty * 4 + i], bs[0][k][tx * 4 + j], acc[0][i][j]);
-          if (kTwo) acc[1][i][j] = fmaf(as[k][ty * 4 + i], bs[1][k][tx * 4 + j], acc[1][i][j]);
-        }
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m >= p.M || n >= p.N) continue;
-      const float v = acc[0][i][j];
-      if (EPI == kEpiGateUp) {
-        const float u = acc[kTwo ? 1 : 0][i][j];
-        if (p.gu) {
-          p.gu[m * 2 * p.N + n] = v;
-          p.gu[m * 2 * p.N + p.N + n] = u;
-        }
-        static_cast<__nv_bfloat16 *>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v / (1.0f + __expf(-v)) * u);
-      } else if (EPI == kEpiStore) {
-        const float a = p.addend ? __bfloat162float(p.addend[m * p.ld_add + n]) : 0.0f;
-        static_cast<__nv_bfloat16 *>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v + a);
-      } else if (EPI == kEpiDact) {
-        const float g = p.gu[m * 2 * p.N + n], u = p.gu[m * 2 * p.N + p.N + n];
-        const float s = 1.0f / (1.0f + __expf(-g));
-        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + m * p.ldo + n;
-        o[0] = __float2bfloat16_rn(v * u * s * (1.0f + g * (1.0f - s)));
-        o[p.N] = __float2bfloat16_rn(v * g * s);
-      } else if (p.mode == kGradBf16) {
-        static_cast<__nv_bfloat16 *>(p.out)[m * p.ldo + n] = __float2bfloat16_rn(v);
-      } else {
-        float *o = static_cast<float *>(p.out) + m * p.ldo + n;
-        *o = p.mode == kGradF32Accumulate ? *o + v : v;
-      }
-    }
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return __fmul_rn(__fdividef(g, __fadd_rn(1.0f, __expf(-g))), u);
 }
 
-template <Epi EPI>
-static bi_status launch_tile(const FfnParams &p, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((p.M + kT - 1) / kT), static_cast<unsigned>((p.N + kT - 1) / kT));
-  return launch_chained(ffn_tile_kernel<EPI>, grid, dim3(256), 0, s, 1, p);
+// 32 bytes to global memory: a whole sector per lane.
+__device__ __forceinline__ void store_32b(void *p, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    uint4 *q = static_cast<uint4 *>(p);
+    q[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    q[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Epilogue of one warp: acc[c] = D[row, col0 + c], c < ncols (a multiple of 16), row = row0 + lane.
+template <FfnEpi EPI>
+__device__ __forceinline__ void ffn_epilogue(const FfnGemm &p, const float (&acc)[128], int row0, int col0, int ncols,
+                                             int lane) {
+  const int limit = min(ncols, p.cols - col0);  // valid columns
+  if constexpr (EPI == kGateUp) {
+    // row0: first of the warp's 16 features; lanes 0-15 hold their gate values, 16-31 their up values
+    const int f = row0 + (lane & 15);
+    const bool is_gate = lane < 16, ok = f < p.rows;
+    __nv_bfloat16 *act = static_cast<__nv_bfloat16 *>(p.out) + static_cast<int64_t>(col0) * p.ldo + f;
+    float *gu = p.gu ? p.gu + static_cast<int64_t>(col0) * 2 * p.rows + (is_gate ? 0 : p.rows) + f : nullptr;
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+      if (c >= limit) break;
+      // the gate lane finishes columns c..c+15, the up lane c+16..c+31
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float mine = is_gate ? acc[c + j] : acc[c + 16 + j];
+        const float other = __shfl_xor_sync(0xffffffffu, is_gate ? acc[c + 16 + j] : acc[c + j], 16);
+        const int t = c + (is_gate ? j : 16 + j);
+        const float g = is_gate ? mine : other, u = is_gate ? other : mine;
+        if (ok && t < limit) act[t * p.ldo] = __float2bfloat16_rn(silu_mul(g, u));
+      }
+      if (gu) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (ok && c + j < limit) gu[static_cast<int64_t>(c + j) * 2 * p.rows] = acc[c + j];
+      }
+    }
+  } else if constexpr (EPI == kStore) {
+    const int f = row0 + lane;
+    if (f >= p.rows) return;
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + static_cast<int64_t>(col0) * p.ldo + f;
+    const __nv_bfloat16 *a = p.addend ? p.addend + static_cast<int64_t>(col0) * p.ld_add + f : nullptr;
+#pragma unroll
+    for (int c = 0; c < 128; c += 16) {
+      if (c >= limit) break;
+      float add[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) add[j] = a && c + j < limit ? __bfloat162float(a[(c + j) * p.ld_add]) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (c + j < limit) o[(c + j) * p.ldo] = __float2bfloat16_rn(__fadd_rn(acc[c + j], add[j]));
+    }
+  } else if constexpr (EPI == kDact) {
+    const int f = row0 + lane;
+    if (f >= p.rows) return;
+    const int64_t two = 2 * static_cast<int64_t>(p.rows);
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + col0 * two + f;
+    const float *gu = p.gu + col0 * two + f;
+#pragma unroll
+    for (int c = 0; c < 128; c += 16) {
+      if (c >= limit) break;
+      float g[16], u[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        g[j] = c + j < limit ? __ldcs(gu + (c + j) * two) : 0.0f;
+        u[j] = c + j < limit ? __ldcs(gu + (c + j) * two + p.rows) : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float s = __fdividef(1.0f, __fadd_rn(1.0f, __expf(-g[j])));
+        const float d = acc[c + j];
+        if (c + j < limit) {
+          o[(c + j) * two] = __float2bfloat16_rn(d * u[j] * s * (1.0f + g[j] * (1.0f - s)));
+          o[(c + j) * two + p.rows] = __float2bfloat16_rn(d * g[j] * s);
+        }
+      }
+    }
+  } else {
+    const int r = row0 + lane;
+    if (r >= p.rows) return;
+    const int64_t at = static_cast<int64_t>(r) * p.ldo + col0;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+#pragma unroll
+    for (int c = 0; c < 128; c += 16) {  // result columns come in multiples of 16
+      if (c >= limit) break;
+      if (p.mode == kGradBf16) {
+        uint32_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = pack_bf16(acc[c + 2 * j], acc[c + 2 * j + 1]);
+        store_32b(static_cast<__nv_bfloat16 *>(p.out) + at + c, v, wide);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 16; h += 8) {
+          float *o = static_cast<float *>(p.out) + at + c + h;
+          uint32_t v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[j] = __float_as_uint(p.mode == kGradF32Accumulate ? __fadd_rn(o[j], acc[c + h + j]) : acc[c + h + j]);
+          store_32b(o, v, wide);
+        }
+      }
+    }
+  }
+}
+
+template <FfnEpi EPI, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kFThreads, 1)
+    ffn_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ FfnGemm prm) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *tiles = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(tiles + kFStages * kFStageBytes);
+  uint64_t *empty = full + kFStages;
+  uint64_t *tfull = empty + kFStages;  // [2]
+  uint64_t *tempty = tfull + 2;        // [2]
+  uint64_t *drain = tempty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int unit0 = static_cast<int>(cluster_id_x()), nunits = static_cast<int>(num_clusters_x());
+  const int total = prm.m_tiles * prm.n_tiles;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kFStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&tfull[a]), 1);
+      mbar_init(smem_u32(&tempty[a]), 16);  // the epilogue warps of both CTAs, on the even CTA's barrier
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    if (lane == 0) *tmem_slot = 0u;
+    __syncwarp();
+    tmem_alloc_pair(smem_u32(tmem_slot), 2 * kFAccCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+
+  auto wait = [&](uint32_t bar, uint32_t parity, volatile int *ab) { return mbar_wait_cl(bar, parity, ab, prm.err); };
+  // tokens fastest: the tiles of a row block follow one another and share its A in L2
+  auto row_of = [&](int tile) { return (tile / prm.n_tiles) * (EPI == kGateUp ? kFM : 2 * kFM); };
+  auto col_of = [&](int tile) { return (tile % prm.n_tiles) * prm.n; };
+
+  if (warp == 0) {
+    // ---------------------------------------------------- TMA producer --
+    if (elect_one()) {
+      const int half = prm.n / 2;
+      const uint32_t b_bytes = B_MN ? static_cast<uint32_t>((half + 63) / 64 * kFSlab) : static_cast<uint32_t>(half * kFK * 2);
+      int stage = 0;
+      uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
+      bool ok = true;
+      for (int tile = unit0; tile < total && ok; tile += nunits) {
+        const int row = row_of(tile) + static_cast<int>(rank) * (EPI == kGateUp ? kFM / 2 : kFM);
+        const int col = col_of(tile) + static_cast<int>(rank) * half;
+        for (int kb = 0; kb < prm.nkb; ++kb) {
+          if (!wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = smem_u32(tiles + stage * kFStageBytes);
+          const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * (kFABytes + b_bytes));
+          const int k = kb * kFK;
+          if (EPI == kGateUp) {
+            tma_load_4d_pair(st, &tmA, fb, k, 0, 0, row / 16);
+          } else if (A_MN) {
+            tma_load_2d_pair(st, &tmA, fb, row, k);
+            tma_load_2d_pair(st + kFSlab, &tmA, fb, row + 64, k);
+          } else {
+            tma_load_2d_pair(st, &tmA, fb, k, row);
+          }
+          if (B_MN) {
+            tma_load_2d_pair(st + kFABytes, &tmB, fb, col, k);
+            if (half > 64) tma_load_2d_pair(st + kFABytes + kFSlab, &tmB, fb, col + 64, k);
+          } else {
+            tma_load_2d_pair(st + kFABytes, &tmB, fb, k, col);
+          }
+          issued_mask |= 1u << stage;
+          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == kFStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (*abort_flag) {
+        // every copy this CTA started lands before it exits
+        if (rank == 0) {
+          for (int s = 0; s < kFStages; ++s)
+            if ((issued_mask >> s) & 1u) wait(smem_u32(&full[s]), (issued_parity >> s) & 1u, nullptr);
+        }
+        // the odd CTA's copies complete on the even CTA's barriers: give them time to land
+        const unsigned long long t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------ MMA issuer --
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc = idesc_bf16_f32(2 * kFM, prm.n) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      bool ok = true;
+      for (int tile = unit0; tile < total && ok && !*abort_flag; tile += nunits) {
+        for (int kb0 = 0; kb0 < prm.nkb && ok; kb0 += prm.slice_kb) {
+          const int kb1 = min(prm.nkb, kb0 + prm.slice_kb);
+          if (!wait(smem_u32(&tempty[buf]), buf_phase ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + static_cast<uint32_t>(buf * kFAccCols);
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (!wait(smem_u32(&full[stage]), phase, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a0 = smem_u32(tiles + stage * kFStageBytes), b0 = a0 + kFABytes;
+#pragma unroll
+            for (int k = 0; k < kFK / 16; ++k) {
+              const uint64_t ad = A_MN ? sdesc_sw128_mn(a0 + k * 2048, kFSlab) : sdesc_sw128(a0 + k * 32);
+              const uint64_t bd = B_MN ? sdesc_sw128_mn(b0 + k * 2048, kFSlab) : sdesc_sw128(b0 + k * 32);
+              umma_f16_pair(d, ad, bd, idesc, (kb > kb0 || k) ? 1u : 0u);
+            }
+            umma_commit_pair(smem_u32(&empty[stage]), 0x3);
+            if (++stage == kFStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          umma_commit_pair(smem_u32(&tfull[buf]), 0x3);
+          if (++buf == 2) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
+        }
+      }
+      // every MMA into both CTAs' tensor memory has completed
+      umma_commit_pair(smem_u32(drain), 0x3);
+      wait(smem_u32(drain), 0, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------- epilogue --
+    const int q = warp & 3, h = (warp - 2) >> 2;
+    const int ncols = prm.n / 2;  // columns of this warp: half h of the tile
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    bool ok = true;
+    for (int tile = unit0; tile < total && ok; tile += nunits) {
+      float acc[128];
+#pragma unroll
+      for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
+      for (int kb0 = 0; kb0 < prm.nkb; kb0 += prm.slice_kb) {
+        ok = __all_sync(0xffffffffu, wait(smem_u32(&tfull[buf]), buf_phase, abort_flag) ? 1 : 0) != 0;
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                           static_cast<uint32_t>(buf * kFAccCols + h * ncols);
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          if (c < ncols) {
+            uint32_t d[16];
+            tmem_ld16(t + c, d);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[c + j] = __fadd_rn(acc[c + j], __uint_as_float(d[j]));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[buf]), 0));
+        if (++buf == 2) {
+          buf = 0;
+          buf_phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      const int row0 = row_of(tile) + static_cast<int>(rank) * (EPI == kGateUp ? kFM / 2 : kFM) +
+                       q * (EPI == kGateUp ? 16 : 32);
+      ffn_epilogue<EPI>(prm, acc, row0, col_of(tile) + h * ncols, ncols, lane);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // the even CTA's final commit: its last MMAs have left this CTA's memory too
+  if (rank != 0 && threadIdx.x == 32) wait(smem_u32(drain), 0, nullptr);
+  cluster_sync_all();  // neither CTA leaves while the other may still signal its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 2 * kFAccCols);
+  }
+}
+
+// ------------------------------------------------------------------- host --
+template <FfnEpi EPI, bool A_MN, bool B_MN>
+static bi_status launch_ffn(const CUtensorMap &tmA, const CUtensorMap &tmB, FfnGemm p, cudaStream_t s) {
+  static std::mutex mu;
+  static int max_units[64] = {};  // CTA pairs resident at once, per device
+  static ContextSetup setup;      // the shared-memory attribute is per context
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) {
+    set_error("device ordinal %d out of range", dev);
+    return BI_ERR_CUDA;
+  }
+  auto kern = ffn_gemm_kernel<EPI, A_MN, B_MN>;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (max_units[dev] == 0 || setup.pending(dev)) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(2 * (num_sms() / 2));
+      cfg.blockDim = dim3(kFThreads);
+      cfg.dynamicSmemBytes = kFSmem;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFSmem);
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+      if (e != cudaSuccess || clusters <= 0) {
+        cudaGetLastError();
+        set_error("feed-forward kernel set-up: %s (%d clusters)", cudaGetErrorString(e), clusters);
+        return BI_ERR_CUDA;
+      }
+      max_units[dev] = clusters;
+      setup.done(dev);
+    }
+  }
+  p.err = device_error_word();
+  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+  if (tiles > (int64_t(1) << 30)) {
+    set_error("feed-forward product with %lld tiles", (long long)tiles);
+    return BI_ERR_UNSUPPORTED;
+  }
+  const int units = static_cast<int>(std::min<int64_t>(max_units[dev], tiles));
+  return launch_chained(kern, dim3(2 * units), dim3(kFThreads), kFSmem, s, 2, tmA, tmB, p);
+}
+
+static int div_up(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// rows x cols result, reduction length K in slices of `slice`; columns of a
+// tile: at most 256, for fewer tokens their number rounded up to 32 (MN-major
+// B: to 128, its slabs are 64 per CTA).
+static FfnGemm plan(int64_t rows, int64_t cols, int64_t K, int64_t slice, int tile_rows, int n_step) {
+  FfnGemm p{};
+  p.rows = static_cast<int>(rows);
+  p.cols = static_cast<int>(cols);
+  p.n = std::min(256, div_up(cols, n_step) * n_step);
+  p.m_tiles = div_up(rows, tile_rows);
+  p.n_tiles = div_up(cols, p.n);
+  p.nkb = div_up(K, kFK);
+  p.slice_kb = std::max(1, static_cast<int>(slice / kFK));
+  return p;
 }
 
 bi_status launch_ffn_gate_up(Mat x, const __nv_bfloat16 *w13, __nv_bfloat16 *act, float *gu, int64_t M, int64_t H,
                              int64_t I, cudaStream_t s) {
-  FfnParams p{{x.p, x.ld, 1}, {w13, H, 1}, {w13 + I * H, H, 1}, M, I, H, act, I, nullptr, 0, gu, 0};
-  return launch_tile<kEpiGateUp>(p, s);
+  FfnGemm p = plan(I, M, H, kSliceK, kFM, 32);
+  p.out = act;
+  p.ldo = I;
+  p.gu = gu;
+  CUtensorMap a, b;
+  if (!make_tma_inter_bf16(&a, w13, I, I, H) || !make_tma_2d_bf16_ld(&b, x.p, M, H, x.ld, p.n / 2)) return BI_ERR_CUDA;
+  return launch_ffn<kGateUp, false, false>(a, b, p, s);
 }
 
 bi_status launch_ffn_down(const __nv_bfloat16 *act, const __nv_bfloat16 *w2, Mat addend, __nv_bfloat16 *out,
                           int64_t ldo, int64_t M, int64_t H, int64_t I, cudaStream_t s) {
-  FfnParams p{{act, I, 1}, {w2, I, 1}, {}, M, H, I, out, ldo, addend.p, addend.ld, nullptr, 0};
-  return launch_tile<kEpiStore>(p, s);
+  FfnGemm p = plan(H, M, I, kSliceK, 2 * kFM, 32);
+  p.out = out;
+  p.ldo = ldo;
+  p.addend = addend.p;
+  p.ld_add = addend.ld;
+  CUtensorMap a, b;
+  if (!make_tma_2d_bf16(&a, w2, H, I, kFM) || !make_tma_2d_bf16(&b, act, M, I, p.n / 2)) return BI_ERR_CUDA;
+  return launch_ffn<kStore, false, false>(a, b, p, s);
 }
 
 bi_status launch_ffn_dact(Mat dout, const __nv_bfloat16 *w2, const float *gu, __nv_bfloat16 *dgu, int64_t M, int64_t H,
                           int64_t I, cudaStream_t s) {
-  FfnParams p{{dout.p, dout.ld, 1}, {w2, 1, I}, {}, M, I, H, dgu, 2 * I, nullptr, 0, const_cast<float *>(gu), 0};
-  return launch_tile<kEpiDact>(p, s);
+  FfnGemm p = plan(I, M, H, kSliceK, 2 * kFM, 32);
+  p.out = dgu;
+  p.ldo = 2 * I;
+  p.gu = const_cast<float *>(gu);
+  CUtensorMap a, b;
+  if (!make_tma_2d_bf16(&a, w2, H, I, kFK) || !make_tma_2d_bf16_ld(&b, dout.p, M, H, dout.ld, p.n / 2))
+    return BI_ERR_CUDA;
+  return launch_ffn<kDact, true, false>(a, b, p, s);
 }
 
 bi_status launch_ffn_dx(const __nv_bfloat16 *dgu, const __nv_bfloat16 *w13, __nv_bfloat16 *dx, int64_t lddx, int64_t M,
                         int64_t H, int64_t I, cudaStream_t s) {
-  FfnParams p{{dgu, 2 * I, 1}, {w13, 1, H}, {}, M, H, 2 * I, dx, lddx, nullptr, 0, nullptr, 0};
-  return launch_tile<kEpiStore>(p, s);
+  FfnGemm p = plan(H, M, 2 * I, kSliceK, 2 * kFM, 32);
+  p.out = dx;
+  p.ldo = lddx;
+  CUtensorMap a, b;
+  if (!make_tma_2d_bf16(&a, w13, 2 * I, H, kFK) || !make_tma_2d_bf16(&b, dgu, M, 2 * I, p.n / 2)) return BI_ERR_CUDA;
+  return launch_ffn<kStore, true, false>(a, b, p, s);
 }
 
 bi_status launch_ffn_wgrad(Mat a, Mat b, void *dw, int grad_mode, int64_t M, int64_t rows, int64_t cols,
                            cudaStream_t s) {
-  FfnParams p{{a.p, 1, a.ld}, {b.p, 1, b.ld}, {}, rows, cols, M, dw, cols, nullptr, 0, nullptr, grad_mode};
-  return launch_tile<kEpiWgrad>(p, s);
+  FfnGemm p = plan(rows, cols, M, (M + kFK - 1) / kFK * kFK, 2 * kFM, 128);
+  p.out = dw;
+  p.ldo = cols;
+  p.mode = grad_mode;
+  CUtensorMap ta, tb;
+  if (!make_tma_2d_bf16_ld(&ta, a.p, M, rows, a.ld, kFK) || !make_tma_2d_bf16_ld(&tb, b.p, M, cols, b.ld, kFK))
+    return BI_ERR_CUDA;
+  return launch_ffn<kWgrad, true, true>(ta, tb, p, s);
 }
 
 }  // namespace bimoe
