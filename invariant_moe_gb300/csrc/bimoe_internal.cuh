@@ -56,6 +56,9 @@ bool make_tma_inter_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint
 // a [box_rows, 64]-element box, 128-byte swizzle.
 bool make_tma_2d_bf16_ld(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld,
                          uint32_t box_rows);
+// Encode a 2-D byte map over a row-major [rows, row_bytes] array with a
+// [box_rows, 128]-byte box, 128-byte swizzle.
+bool make_tma_2d_u8(CUtensorMap *map, const void *base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows);
 bool make_tma_2d_f32(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                      uint32_t box_rows);
 void set_error(const char *fmt, ...);
@@ -417,6 +420,14 @@ __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// Untiled copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
+// to this CTA's shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 // ---- tcgen05 (5th-generation tensor cores, tensor memory)
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
@@ -445,6 +456,26 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint6
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// D (+)= A * B^T over 64 values of k, kind::mxf4: E2M1 operands in shared
+// memory, one E8M0 scale for each 32 k of a row in tensor memory, fp32
+// accumulate.  The scale words of 128 rows hold 128 k (four bytes); the
+// instruction descriptor says which two bytes this step uses.
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+// Copy a 512-byte scale tile (32 lanes x 16 bytes) from shared memory to four
+// tensor-memory columns, repeated in the four lane quarters.  Ordered before
+// the MMAs that the same thread issues after it and behind those before it.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t s_desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
 }
 // Arrive once on an mbarrier when every previously issued tcgen05.mma of this
 // thread has completed.
@@ -547,6 +578,24 @@ __device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t slab
   d |= static_cast<uint64_t>(1) << 46;
   d |= static_cast<uint64_t>(2) << 61;
   return d;
+}
+
+// Descriptor of a 512-byte scale tile: no swizzle, 8-row groups of 16-byte
+// rows 128 B apart.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(128 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+
+// Instruction descriptor of tcgen05.mma kind::mxf4: E2M1 operands (K-major),
+// E8M0 scales, shape M x N; `half` (0 or 1) picks the scale bytes 0-1 or 2-3
+// of both operands' scale words.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, uint32_t half) {
+  return (2u * half << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+         (static_cast<uint32_t>(m >> 4) << 24) | (2u * half << 29);
 }
 
 // Instruction-descriptor bits that mark A / B as MN-major (kind::f16).
