@@ -518,29 +518,67 @@ def moe_layer(x_bf16, w_router, w13, w2, top_k, bias=None, stream=None):
 
 
 # ------------------------------------ dense gated feed-forward block --
-def _rows(t, dtype, name, shape, device=None):
-    """(pointer, row stride) of a 2-D tensor with unit column stride."""
+_BF, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_fns = {}
+
+
+def _launch(name, device, stream, *args):
+    """Calls a stream-ordered entry point on device number ``device``: on
+    ``stream``, or on that device's current stream, with the device current."""
+    if device != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return _launch(name, device, stream, *args)
+    f = _fns.get(name)
+    if f is None:
+        f = _fns[name] = getattr(load_library(), name)
+    st = f(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
+    if st != BI_OK:
+        raise BimoeError(name, st, load_library().bi_last_error_message().decode())
+
+
+def _device_of(t, name):
+    """Device number of a CUDA tensor (checked once per call, the other tensors against it)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    return t.get_device()
+
+
+def _flat(t, dtype, name, device):
+    """Address of a contiguous tensor on device number ``device``."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, dtype, name, torch.device("cuda", device)).value  # says what is wrong
+
+
+def _rows(t, dtype, name, rows, cols, device):
+    """(address, row stride) of a [rows, cols] tensor with unit column stride on device number ``device``."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be {[rows, cols]}, got {list(t.shape)}")
+    if rows <= 1:
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have unit column stride")
+        return t.data_ptr(), cols
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else shape[1])
+    return t.data_ptr(), ld
 
 
 def _check_ffn_shapes(x, w13, w2):
     if x.dim() != 2 or w13.dim() != 2 or w2.dim() != 2:
         raise ValueError("x, w13 and w2 must be 2-D")
     M, H = x.shape
-    I = w2.shape[1]
-    if tuple(w13.shape) != (2 * I, H) or w2.shape[0] != H:
+    H2, I = w2.shape
+    if w13.shape != (2 * I, H) or H2 != H:
         raise ValueError("w13 must be [2I, H] and w2 [H, I]")
     return M, H, I
 
@@ -549,50 +587,49 @@ def ffn_workspace(M, H, I, device):
     """Workspace of bi_ffn_forward and bi_ffn_backward at these sizes."""
     n = int(load_library().bi_ffn_workspace_bytes(M, H, I))
     if n == 0:
-        raise ValueError("unsupported feed-forward sizes")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+        raise ValueError("unsupported feed-forward sizes: " + load_library().bi_last_error_message().decode())
+    return torch.empty(n, dtype=_U8, device=device)
 
 
 def ffn_saved(M, I, device):
     """(gu fp32 [M, 2I], act bf16 [M, I]): what bi_ffn_forward_train keeps for bi_ffn_backward."""
-    return (torch.empty(M, 2 * I, dtype=torch.float32, device=device),
-            torch.empty(M, I, dtype=torch.bfloat16, device=device))
+    return torch.empty(M, 2 * I, dtype=_F32, device=device), torch.empty(M, I, dtype=_BF, device=device)
 
 
 def bi_ffn_forward(x, w13, w2, addend=None, out=None, workspace=None, stream=None):
     """out [M,H] bf16 = (silu(x Wg^T) * (x Wu^T)) W2^T (+ addend), w13 [2I,H] = [Wg; Wu],
     w2 [H,I]; x, addend and out may be rows of wider tensors (row stride a multiple of 8)."""
     M, H, I = _check_ffn_shapes(x, w13, w2)
-    dev, bf = x.device, torch.bfloat16
-    px, ldx = _rows(x, bf, "x", (M, H))
-    pa, lda = _rows(addend, bf, "addend", (M, H), dev) if addend is not None else (None, 0)
+    dev = _device_of(x, "x")
+    px, ldx = _rows(x, _BF, "x", M, H, dev)
+    pa, lda = _rows(addend, _BF, "addend", M, H, dev) if addend is not None else (None, 0)
     if out is None:
-        out = torch.empty(M, H, dtype=bf, device=dev)
-    po, ldo = _rows(out, bf, "out", (M, H), dev)
+        out = torch.empty(M, H, dtype=_BF, device=x.device)
+    po, ldo = _rows(out, _BF, "out", M, H, dev)
     if workspace is None:
-        workspace = ffn_workspace(M, H, I, dev)
-    _call("bi_ffn_forward", px, ldx, _ptr(w13, bf, "w13", dev), _ptr(w2, bf, "w2", dev), pa, lda, po, ldo, M, H, I,
-          _ptr(workspace, torch.uint8, "workspace", dev), workspace.numel(), _stream(stream))
+        workspace = ffn_workspace(M, H, I, x.device)
+    _launch("bi_ffn_forward", dev, stream, px, ldx, _flat(w13, _BF, "w13", dev), _flat(w2, _BF, "w2", dev), pa, lda,
+            po, ldo, M, H, I, _flat(workspace, _U8, "workspace", dev), workspace.numel())
     return out
 
 
 def bi_ffn_forward_train(x, w13, w2, addend=None, out=None, gu=None, act=None, stream=None):
     """bi_ffn_forward that keeps what bi_ffn_backward reads.  Returns (out, gu fp32 [M,2I], act bf16 [M,I])."""
     M, H, I = _check_ffn_shapes(x, w13, w2)
-    dev, bf = x.device, torch.bfloat16
-    px, ldx = _rows(x, bf, "x", (M, H))
-    pa, lda = _rows(addend, bf, "addend", (M, H), dev) if addend is not None else (None, 0)
+    dev = _device_of(x, "x")
+    px, ldx = _rows(x, _BF, "x", M, H, dev)
+    pa, lda = _rows(addend, _BF, "addend", M, H, dev) if addend is not None else (None, 0)
     if out is None:
-        out = torch.empty(M, H, dtype=bf, device=dev)
-    po, ldo = _rows(out, bf, "out", (M, H), dev)
+        out = torch.empty(M, H, dtype=_BF, device=x.device)
+    po, ldo = _rows(out, _BF, "out", M, H, dev)
     if gu is None:
-        gu = torch.empty(M, 2 * I, dtype=torch.float32, device=dev)
+        gu = torch.empty(M, 2 * I, dtype=_F32, device=x.device)
     if act is None:
-        act = torch.empty(M, I, dtype=bf, device=dev)
-    if tuple(gu.shape) != (M, 2 * I) or tuple(act.shape) != (M, I):
+        act = torch.empty(M, I, dtype=_BF, device=x.device)
+    if gu.shape != (M, 2 * I) or act.shape != (M, I):
         raise ValueError("gu must be [M, 2I] and act [M, I]")
-    _call("bi_ffn_forward_train", px, ldx, _ptr(w13, bf, "w13", dev), _ptr(w2, bf, "w2", dev), pa, lda, po, ldo,
-          _ptr(gu, torch.float32, "gu", dev), _ptr(act, bf, "act", dev), M, H, I, _stream(stream))
+    _launch("bi_ffn_forward_train", dev, stream, px, ldx, _flat(w13, _BF, "w13", dev), _flat(w2, _BF, "w2", dev), pa,
+            lda, po, ldo, _flat(gu, _F32, "gu", dev), _flat(act, _BF, "act", dev), M, H, I)
     return out, gu, act
 
 
@@ -602,32 +639,40 @@ def bi_ffn_backward(dout, x, w13, w2, gu, act, dx=None, dw13=None, dw2=None, nee
     are bf16 (the default) or both fp32; with ``accumulate`` the gradients are added to the fp32
     tensors given."""
     M, H, I = _check_ffn_shapes(x, w13, w2)
-    dev, bf = x.device, torch.bfloat16
-    pdo, lddo = _rows(dout, bf, "dout", (M, H), dev)
-    px, ldx = _rows(x, bf, "x", (M, H))
-    if tuple(gu.shape) != (M, 2 * I) or tuple(act.shape) != (M, I):
+    dev = _device_of(x, "x")
+    px, ldx = _rows(x, _BF, "x", M, H, dev)
+    pdo, lddo = _rows(dout, _BF, "dout", M, H, dev)
+    if gu.shape != (M, 2 * I) or act.shape != (M, I):
         raise ValueError("gu must be [M, 2I] and act [M, I]")
-    wd = next((t.dtype for t, n in ((dw13, need[1]), (dw2, need[2])) if n and t is not None), bf)
-    if wd not in (bf, torch.float32):
+    wd = next((t.dtype for t, n in ((dw13, need[1]), (dw2, need[2])) if n and t is not None), _BF)
+    if wd not in (_BF, _F32):
         raise TypeError(f"dw13 and dw2 must be bfloat16 or float32, got {wd}")
-    if accumulate and (wd != torch.float32 or (need[1] and dw13 is None) or (need[2] and dw2 is None)):
+    if accumulate and (wd != _F32 or (need[1] and dw13 is None) or (need[2] and dw2 is None)):
         raise ValueError("accumulate needs the fp32 tensors that the gradients are added to")
-    if need[0] and dx is None:
-        dx = torch.empty(M, H, dtype=bf, device=dev)
-    if need[1] and dw13 is None:
-        dw13 = torch.empty(2 * I, H, dtype=wd, device=dev)
-    if need[2] and dw2 is None:
-        dw2 = torch.empty(H, I, dtype=wd, device=dev)
-    pdx, lddx = _rows(dx, bf, "dx", (M, H), dev) if need[0] else (None, 0)
-    if need[1] and tuple(dw13.shape) != (2 * I, H) or need[2] and tuple(dw2.shape) != (H, I):
-        raise ValueError("dw13 must be [2I, H] and dw2 [H, I]")
+    pdx = p13 = p2 = None
+    lddx = 0
+    if need[0]:
+        if dx is None:
+            dx = torch.empty(M, H, dtype=_BF, device=x.device)
+        pdx, lddx = _rows(dx, _BF, "dx", M, H, dev)
+    if need[1]:
+        if dw13 is None:
+            dw13 = torch.empty(2 * I, H, dtype=wd, device=x.device)
+        if dw13.shape != (2 * I, H):
+            raise ValueError("dw13 must be [2I, H]")
+        p13 = _flat(dw13, wd, "dw13", dev)
+    if need[2]:
+        if dw2 is None:
+            dw2 = torch.empty(H, I, dtype=wd, device=x.device)
+        if dw2.shape != (H, I):
+            raise ValueError("dw2 must be [H, I]")
+        p2 = _flat(dw2, wd, "dw2", dev)
     if workspace is None:
-        workspace = ffn_workspace(M, H, I, dev)
-    mode = 0 if wd == bf else (2 if accumulate else 1)
-    _call("bi_ffn_backward", pdo, lddo, px, ldx, _ptr(w13, bf, "w13", dev), _ptr(w2, bf, "w2", dev),
-          _ptr(gu, torch.float32, "gu", dev), _ptr(act, bf, "act", dev), pdx, lddx,
-          _ptr(dw13, wd, "dw13", dev) if need[1] else None, _ptr(dw2, wd, "dw2", dev) if need[2] else None, mode,
-          M, H, I, _ptr(workspace, torch.uint8, "workspace", dev), workspace.numel(), _stream(stream))
+        workspace = ffn_workspace(M, H, I, x.device)
+    mode = 0 if wd is _BF else (2 if accumulate else 1)
+    _launch("bi_ffn_backward", dev, stream, pdo, lddo, px, ldx, _flat(w13, _BF, "w13", dev), _flat(w2, _BF, "w2", dev),
+            _flat(gu, _F32, "gu", dev), _flat(act, _BF, "act", dev), pdx, lddx, p13, p2, mode, M, H, I,
+            _flat(workspace, _U8, "workspace", dev), workspace.numel())
     return dx if need[0] else None, dw13 if need[1] else None, dw2 if need[2] else None
 
 
@@ -639,15 +684,15 @@ def mx4_scale_shape(R, K):
 
 def mx4_empty(R, K, device):
     """(codes uint8 [R, K/2], scale tiles uint8): uninitialised buffers for bi_mx4_quantize."""
-    return (torch.empty(R, K // 2, dtype=torch.uint8, device=device),
-            torch.empty(mx4_scale_shape(R, K), dtype=torch.uint8, device=device))
+    return (torch.empty(R, K // 2, dtype=_U8, device=device),
+            torch.empty(mx4_scale_shape(R, K), dtype=_U8, device=device))
 
 
 def mx4_tile_scales(s):
     """Row-major E8M0 scales uint8 [R, K/32] (as checkpoints hold them) in the tiled layout."""
     R, n = s.shape
     rt, kt = (R + 127) // 128, (n + 3) // 4
-    p = torch.zeros(rt * 128, kt * 4, dtype=torch.uint8, device=s.device)
+    p = torch.zeros(rt * 128, kt * 4, dtype=_U8, device=s.device)
     p[:R, :n] = s
     return p.view(rt, 4, 32, kt, 4).permute(0, 3, 2, 1, 4).reshape(rt, kt, 512).contiguous()
 
@@ -666,15 +711,15 @@ def mx4_interleave_gate_up(w13):
     return w13.view(2, I // 16, 16, *w13.shape[1:]).transpose(0, 1).reshape(w13.shape).contiguous()
 
 
-def _mx4_operand(q, s, name, device=None):
-    """(pointers, rows, K) of a quantised matrix."""
-    pq = _ptr(q, torch.uint8, name + " codes", device)
+def _mx4_operand(q, s, name, device):
+    """(addresses, rows, K) of a quantised matrix on device number ``device``."""
+    pq, ps = _flat(q, _U8, name + " codes", device), _flat(s, _U8, name + " scales", device)
     if q.dim() != 2:
         raise ValueError(f"{name} codes must be [rows, K/2]")
-    R, K = q.shape[0], 2 * q.shape[1]
-    if tuple(s.shape) != mx4_scale_shape(R, K):
-        raise ValueError(f"{name} scales must be {list(mx4_scale_shape(R, K))}, got {list(s.shape)}")
-    return pq, _ptr(s, torch.uint8, name + " scales", q.device), R, K
+    R, half = q.shape
+    if s.shape != ((R + 127) // 128, (half + 63) // 64, 512):
+        raise ValueError(f"{name} scales must be {list(mx4_scale_shape(R, 2 * half))}, got {list(s.shape)}")
+    return pq, ps, R, 2 * half
 
 
 def bi_mx4_quantize(x, q=None, scales=None, stream=None):
@@ -684,54 +729,56 @@ def bi_mx4_quantize(x, q=None, scales=None, stream=None):
     R, K = x.shape
     if K % 32:
         raise ValueError("K must be a multiple of 32")
-    f32 = x.dtype == torch.float32
-    px, ldx = _rows(x, torch.float32 if f32 else torch.bfloat16, "x", (R, K))
+    dev = _device_of(x, "x")
+    f32 = x.dtype is _F32
+    px, ldx = _rows(x, _F32 if f32 else _BF, "x", R, K, dev)
     if q is None or scales is None:
         nq, ns = mx4_empty(R, K, x.device)
         q, scales = nq if q is None else q, ns if scales is None else scales
-    if tuple(q.shape) != (R, K // 2):
+    pq, ps, R2, K2 = _mx4_operand(q, scales, "q", dev)
+    if R2 != R or K2 != K:
         raise ValueError("q must be [R, K/2]")
-    pq, ps, _, _ = _mx4_operand(q, scales, "q", x.device)
-    _call("bi_mx4_quantize", px, int(f32), ldx, pq, ps, R, K, _stream(stream))
+    _launch("bi_mx4_quantize", dev, stream, px, f32, ldx, pq, ps, R, K)
     return q, scales
 
 
 def bi_mx4_dequantize(q, scales, out=None, dtype=torch.bfloat16, stream=None):
     """The values [R,K] (bf16 or fp32, both exact) that codes and scale tiles stand for."""
-    pq, ps, R, K = _mx4_operand(q, scales, "q")
+    dev = _device_of(q, "q codes")
+    pq, ps, R, K = _mx4_operand(q, scales, "q", dev)
     if out is None:
         out = torch.empty(R, K, dtype=dtype, device=q.device)
-    f32 = out.dtype == torch.float32
-    po, ldo = _rows(out, torch.float32 if f32 else torch.bfloat16, "out", (R, K), q.device)
-    _call("bi_mx4_dequantize", pq, ps, po, int(f32), ldo, R, K, _stream(stream))
+    f32 = out.dtype is _F32
+    po, ldo = _rows(out, _F32 if f32 else _BF, "out", R, K, dev)
+    _launch("bi_mx4_dequantize", dev, stream, pq, ps, po, f32, ldo, R, K)
     return out
 
 
 def bi_mx4_gemm(xq, xs, wq, ws, addend=None, out=None, stream=None):
     """out [M,N] bf16 = X W^T (+ addend) of two quantised matrices X [M,K], W [N,K]."""
-    px, pxs, M, K = _mx4_operand(xq, xs, "x")
-    dev = xq.device
+    dev = _device_of(xq, "x codes")
+    px, pxs, M, K = _mx4_operand(xq, xs, "x", dev)
     pw, pws, N, K2 = _mx4_operand(wq, ws, "w", dev)
     if K2 != K:
         raise ValueError("x and w must have the same K")
-    pa, lda = _rows(addend, torch.bfloat16, "addend", (M, N), dev) if addend is not None else (None, 0)
+    pa, lda = _rows(addend, _BF, "addend", M, N, dev) if addend is not None else (None, 0)
     if out is None:
-        out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-    po, ldo = _rows(out, torch.bfloat16, "out", (M, N), dev)
-    _call("bi_mx4_gemm", px, pxs, pw, pws, pa, lda, po, ldo, M, N, K, _stream(stream))
+        out = torch.empty(M, N, dtype=_BF, device=xq.device)
+    po, ldo = _rows(out, _BF, "out", M, N, dev)
+    _launch("bi_mx4_gemm", dev, stream, px, pxs, pw, pws, pa, lda, po, ldo, M, N, K)
     return out
 
 
 def bi_mx4_gate_up(xq, xs, w13q, w13s, out=None, stream=None):
     """act [M,I] bf16 = silu(X Wg^T) * (X Wu^T), the weight's rows interleaved by mx4_interleave_gate_up
     before they were quantised."""
-    px, pxs, M, K = _mx4_operand(xq, xs, "x")
-    dev = xq.device
+    dev = _device_of(xq, "x codes")
+    px, pxs, M, K = _mx4_operand(xq, xs, "x", dev)
     pw, pws, N, K2 = _mx4_operand(w13q, w13s, "w13", dev)
     if K2 != K or N % 32:
         raise ValueError("x and w13 must have the same K, and w13 2I rows, I a multiple of 16")
     if out is None:
-        out = torch.empty(M, N // 2, dtype=torch.bfloat16, device=dev)
-    po, ldo = _rows(out, torch.bfloat16, "out", (M, N // 2), dev)
-    _call("bi_mx4_gate_up", px, pxs, pw, pws, po, ldo, M, N // 2, K, _stream(stream))
+        out = torch.empty(M, N // 2, dtype=_BF, device=xq.device)
+    po, ldo = _rows(out, _BF, "out", M, N // 2, dev)
+    _launch("bi_mx4_gate_up", dev, stream, px, pxs, pw, pws, po, ldo, M, N // 2, K)
     return out

@@ -41,7 +41,10 @@ constexpr int kFBBytes = 128 * kFK * 2;        // 16 KB: at most 128 rows of B p
 constexpr int kFStageBytes = kFABytes + kFBBytes;
 constexpr int kFSlab = 64 * kFK * 2;           // an MN-major slab: 64 rows or columns x 64 k
 constexpr int kFAccCols = 256;
-constexpr int kFThreads = 320;                 // TMA, MMA, 8 epilogue warps
+constexpr int kFThreads = 384;                 // TMA and MMA warps (two idle), 8 epilogue warps
+// registers a thread: 168 at launch (384 x 168 = 64512); the first four warps
+// hand theirs to the epilogue's, 128 x 40 + 256 x 232 = 64512
+constexpr int kFRegsFew = 40, kFRegsMany = 232;
 constexpr int kFSmem = 1024 + kFStages * kFStageBytes + 256;
 constexpr int kSliceK = 1024;                  // reduction slice of the recipe
 static_assert(kFSmem <= 227 * 1024, "shared memory");
@@ -115,41 +118,60 @@ __device__ __forceinline__ void ffn_epilogue(const FfnGemm &p, const float (&acc
     }
   } else if constexpr (EPI == kStore) {
     const int f = row0 + lane;
-    if (f >= p.rows) return;
+    if (f >= p.rows || limit <= 0) return;
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + static_cast<int64_t>(col0) * p.ldo + f;
-    const __nv_bfloat16 *a = p.addend ? p.addend + static_cast<int64_t>(col0) * p.ld_add + f : nullptr;
+    if (p.addend) {
+      // the next 16 columns' addends are loaded while these are stored; columns
+      // past the last token load the last one's (no branch between the loads)
+      const __nv_bfloat16 *a = p.addend + static_cast<int64_t>(col0) * p.ld_add + f;
+      __nv_bfloat16 add[2][16];
 #pragma unroll
-    for (int c = 0; c < 128; c += 16) {
-      if (c >= limit) break;
-      float add[16];
+      for (int j = 0; j < 16; ++j) add[0][j] = a[min(j, limit - 1) * p.ld_add];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) add[j] = a && c + j < limit ? __bfloat162float(a[(c + j) * p.ld_add]) : 0.0f;
+      for (int c = 0; c < 128; c += 16) {
+        if (c >= limit) break;
+        if (c + 16 < limit) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (c + j < limit) o[(c + j) * p.ldo] = __float2bfloat16_rn(__fadd_rn(acc[c + j], add[j]));
+          for (int j = 0; j < 16; ++j) add[(c / 16 + 1) & 1][j] = a[min(c + 16 + j, limit - 1) * p.ld_add];
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (c + j < limit)
+            o[(c + j) * p.ldo] = __float2bfloat16_rn(__fadd_rn(acc[c + j], __bfloat162float(add[(c / 16) & 1][j])));
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 128; ++c)
+        if (c < limit) o[c * p.ldo] = __float2bfloat16_rn(acc[c]);
     }
   } else if constexpr (EPI == kDact) {
     const int f = row0 + lane;
-    if (f >= p.rows) return;
+    if (f >= p.rows || limit <= 0) return;
     const int64_t two = 2 * static_cast<int64_t>(p.rows);
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + col0 * two + f;
     const float *gu = p.gu + col0 * two + f;
+    float g[2][16], u[2][16];
+    auto load = [&](int c, float (&gv)[16], float (&uv)[16]) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float *at = gu + min(c + j, limit - 1) * two;
+        gv[j] = __ldcs(at);
+        uv[j] = __ldcs(at + p.rows);
+      }
+    };
+    load(0, g[0], u[0]);
 #pragma unroll
     for (int c = 0; c < 128; c += 16) {
       if (c >= limit) break;
-      float g[16], u[16];
+      if (c + 16 < limit) load(c + 16, g[(c / 16 + 1) & 1], u[(c / 16 + 1) & 1]);
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        g[j] = c + j < limit ? __ldcs(gu + (c + j) * two) : 0.0f;
-        u[j] = c + j < limit ? __ldcs(gu + (c + j) * two + p.rows) : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float s = __fdividef(1.0f, __fadd_rn(1.0f, __expf(-g[j])));
+        const float gv = g[(c / 16) & 1][j], uv = u[(c / 16) & 1][j];
+        const float s = __fdividef(1.0f, __fadd_rn(1.0f, __expf(-gv)));
         const float d = acc[c + j];
         if (c + j < limit) {
-          o[(c + j) * two] = __float2bfloat16_rn(d * u[j] * s * (1.0f + g[j] * (1.0f - s)));
-          o[(c + j) * two + p.rows] = __float2bfloat16_rn(d * g[j] * s);
+          o[(c + j) * two] = __float2bfloat16_rn(d * uv * s * (1.0f + gv * (1.0f - s)));
+          o[(c + j) * two + p.rows] = __float2bfloat16_rn(d * gv * s);
         }
       }
     }
@@ -234,112 +256,116 @@ __global__ void __launch_bounds__(kFThreads, 1)
   auto row_of = [&](int tile) { return (tile / prm.n_tiles) * (EPI == kGateUp ? kFM : 2 * kFM); };
   auto col_of = [&](int tile) { return (tile % prm.n_tiles) * prm.n; };
 
-  if (warp == 0) {
-    // ---------------------------------------------------- TMA producer --
-    if (elect_one()) {
-      const int half = prm.n / 2;
-      const uint32_t b_bytes = B_MN ? static_cast<uint32_t>((half + 63) / 64 * kFSlab) : static_cast<uint32_t>(half * kFK * 2);
-      int stage = 0;
-      uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
-      bool ok = true;
-      for (int tile = unit0; tile < total && ok; tile += nunits) {
-        const int row = row_of(tile) + static_cast<int>(rank) * (EPI == kGateUp ? kFM / 2 : kFM);
-        const int col = col_of(tile) + static_cast<int>(rank) * half;
-        for (int kb = 0; kb < prm.nkb; ++kb) {
-          if (!wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = smem_u32(tiles + stage * kFStageBytes);
-          const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * (kFABytes + b_bytes));
-          const int k = kb * kFK;
-          if (EPI == kGateUp) {
-            tma_load_4d_pair(st, &tmA, fb, k, 0, 0, row / 16);
-          } else if (A_MN) {
-            tma_load_2d_pair(st, &tmA, fb, row, k);
-            tma_load_2d_pair(st + kFSlab, &tmA, fb, row + 64, k);
-          } else {
-            tma_load_2d_pair(st, &tmA, fb, k, row);
-          }
-          if (B_MN) {
-            tma_load_2d_pair(st + kFABytes, &tmB, fb, col, k);
-            if (half > 64) tma_load_2d_pair(st + kFABytes + kFSlab, &tmB, fb, col + 64, k);
-          } else {
-            tma_load_2d_pair(st + kFABytes, &tmB, fb, k, col);
-          }
-          issued_mask |= 1u << stage;
-          issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == kFStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
-      if (*abort_flag) {
-        // every copy this CTA started lands before it exits
-        if (rank == 0) {
-          for (int s = 0; s < kFStages; ++s)
-            if ((issued_mask >> s) & 1u) wait(smem_u32(&full[s]), (issued_parity >> s) & 1u, nullptr);
-        }
-        // the odd CTA's copies complete on the even CTA's barriers: give them time to land
-        const unsigned long long t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 200000ull) {
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------ MMA issuer --
-    if (rank == 0 && elect_one()) {
-      const uint32_t idesc = idesc_bf16_f32(2 * kFM, prm.n) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, buf_phase = 0;
-      bool ok = true;
-      for (int tile = unit0; tile < total && ok && !*abort_flag; tile += nunits) {
-        for (int kb0 = 0; kb0 < prm.nkb && ok; kb0 += prm.slice_kb) {
-          const int kb1 = min(prm.nkb, kb0 + prm.slice_kb);
-          if (!wait(smem_u32(&tempty[buf]), buf_phase ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d = tmem_base + static_cast<uint32_t>(buf * kFAccCols);
-          for (int kb = kb0; kb < kb1; ++kb) {
-            if (!wait(smem_u32(&full[stage]), phase, abort_flag)) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFRegsFew));
+    if (warp == 0) {
+      // ---------------------------------------------------- TMA producer --
+      if (elect_one()) {
+        const int half = prm.n / 2;
+        const uint32_t b_bytes = B_MN ? static_cast<uint32_t>((half + 63) / 64 * kFSlab) : static_cast<uint32_t>(half * kFK * 2);
+        int stage = 0;
+        uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
+        bool ok = true;
+        for (int tile = unit0; tile < total && ok; tile += nunits) {
+          const int row = row_of(tile) + static_cast<int>(rank) * (EPI == kGateUp ? kFM / 2 : kFM);
+          const int col = col_of(tile) + static_cast<int>(rank) * half;
+          for (int kb = 0; kb < prm.nkb; ++kb) {
+            if (!wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
               ok = false;
               break;
             }
-            tc_fence_after();
-            const uint32_t a0 = smem_u32(tiles + stage * kFStageBytes), b0 = a0 + kFABytes;
-#pragma unroll
-            for (int k = 0; k < kFK / 16; ++k) {
-              const uint64_t ad = A_MN ? sdesc_sw128_mn(a0 + k * 2048, kFSlab) : sdesc_sw128(a0 + k * 32);
-              const uint64_t bd = B_MN ? sdesc_sw128_mn(b0 + k * 2048, kFSlab) : sdesc_sw128(b0 + k * 32);
-              umma_f16_pair(d, ad, bd, idesc, (kb > kb0 || k) ? 1u : 0u);
+            const uint32_t st = smem_u32(tiles + stage * kFStageBytes);
+            const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * (kFABytes + b_bytes));
+            const int k = kb * kFK;
+            if (EPI == kGateUp) {
+              tma_load_4d_pair(st, &tmA, fb, k, 0, 0, row / 16);
+            } else if (A_MN) {
+              tma_load_2d_pair(st, &tmA, fb, row, k);
+              tma_load_2d_pair(st + kFSlab, &tmA, fb, row + 64, k);
+            } else {
+              tma_load_2d_pair(st, &tmA, fb, k, row);
             }
-            umma_commit_pair(smem_u32(&empty[stage]), 0x3);
+            if (B_MN) {
+              tma_load_2d_pair(st + kFABytes, &tmB, fb, col, k);
+              if (half > 64) tma_load_2d_pair(st + kFABytes + kFSlab, &tmB, fb, col + 64, k);
+            } else {
+              tma_load_2d_pair(st + kFABytes, &tmB, fb, k, col);
+            }
+            issued_mask |= 1u << stage;
+            issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
             if (++stage == kFStages) {
               stage = 0;
               phase ^= 1u;
             }
           }
-          if (!ok) break;
-          umma_commit_pair(smem_u32(&tfull[buf]), 0x3);
-          if (++buf == 2) {
-            buf = 0;
-            buf_phase ^= 1u;
+        }
+        if (*abort_flag) {
+          // every copy this CTA started lands before it exits
+          if (rank == 0) {
+            for (int s = 0; s < kFStages; ++s)
+              if ((issued_mask >> s) & 1u) wait(smem_u32(&full[s]), (issued_parity >> s) & 1u, nullptr);
+          }
+          // the odd CTA's copies complete on the even CTA's barriers: give them time to land
+          const unsigned long long t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < 200000ull) {
           }
         }
       }
-      // every MMA into both CTAs' tensor memory has completed
-      umma_commit_pair(smem_u32(drain), 0x3);
-      wait(smem_u32(drain), 0, nullptr);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ------------------------------------------------------ MMA issuer --
+      if (rank == 0 && elect_one()) {
+        const uint32_t idesc = idesc_bf16_f32(2 * kFM, prm.n) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, buf_phase = 0;
+        bool ok = true;
+        for (int tile = unit0; tile < total && ok && !*abort_flag; tile += nunits) {
+          for (int kb0 = 0; kb0 < prm.nkb && ok; kb0 += prm.slice_kb) {
+            const int kb1 = min(prm.nkb, kb0 + prm.slice_kb);
+            if (!wait(smem_u32(&tempty[buf]), buf_phase ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem_base + static_cast<uint32_t>(buf * kFAccCols);
+            for (int kb = kb0; kb < kb1; ++kb) {
+              if (!wait(smem_u32(&full[stage]), phase, abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t a0 = smem_u32(tiles + stage * kFStageBytes), b0 = a0 + kFABytes;
+#pragma unroll
+              for (int k = 0; k < kFK / 16; ++k) {
+                const uint64_t ad = A_MN ? sdesc_sw128_mn(a0 + k * 2048, kFSlab) : sdesc_sw128(a0 + k * 32);
+                const uint64_t bd = B_MN ? sdesc_sw128_mn(b0 + k * 2048, kFSlab) : sdesc_sw128(b0 + k * 32);
+                umma_f16_pair(d, ad, bd, idesc, (kb > kb0 || k) ? 1u : 0u);
+              }
+              umma_commit_pair(smem_u32(&empty[stage]), 0x3);
+              if (++stage == kFStages) {
+                stage = 0;
+                phase ^= 1u;
+              }
+            }
+            if (!ok) break;
+            umma_commit_pair(smem_u32(&tfull[buf]), 0x3);
+            if (++buf == 2) {
+              buf = 0;
+              buf_phase ^= 1u;
+            }
+          }
+        }
+        // every MMA into both CTAs' tensor memory has completed
+        umma_commit_pair(smem_u32(drain), 0x3);
+        wait(smem_u32(drain), 0, nullptr);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFRegsMany));
     // -------------------------------------------------------- epilogue --
-    const int q = warp & 3, h = (warp - 2) >> 2;
+    const int q = warp & 3, h = (warp - 4) >> 2;
     const int ncols = prm.n / 2;  // columns of this warp: half h of the tile
     int buf = 0;
     uint32_t buf_phase = 0;
@@ -440,15 +466,26 @@ static bi_status launch_ffn(const CUtensorMap &tmA, const CUtensorMap &tmB, FfnG
 
 static int div_up(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-// rows x cols result, reduction length K in slices of `slice`; columns of a
-// tile: at most 256, for fewer tokens their number rounded up to 32 (MN-major
-// B: to 128, its slabs are 64 per CTA).
-static FfnGemm plan(int64_t rows, int64_t cols, int64_t K, int64_t slice, int tile_rows, int n_step) {
+// rows x cols result, reduction length K in slices of `slice`.  Columns of a
+// tile: the multiple of 32 up to 256 with the least time by a simple model:
+// waves of tiles over the CTA pairs, each as long as its columns plus a
+// constant (what a tile costs besides its MMAs, and that narrow MMAs do not
+// run faster than about 64 columns' time).
+static FfnGemm plan(int64_t rows, int64_t cols, int64_t K, int64_t slice, int tile_rows) {
   FfnGemm p{};
   p.rows = static_cast<int>(rows);
   p.cols = static_cast<int>(cols);
-  p.n = std::min(256, div_up(cols, n_step) * n_step);
   p.m_tiles = div_up(rows, tile_rows);
+  const int64_t pairs = std::max(1, num_sms() / 2);
+  int64_t best = INT64_MAX;
+  for (int n = 256; n >= 32; n -= 32) {
+    const int64_t tiles = static_cast<int64_t>(p.m_tiles) * div_up(cols, n);
+    const int64_t cost = (tiles + pairs - 1) / pairs * (std::max(n, 64) + 16);
+    if (cost < best) {
+      best = cost;
+      p.n = n;
+    }
+  }
   p.n_tiles = div_up(cols, p.n);
   p.nkb = div_up(K, kFK);
   p.slice_kb = std::max(1, static_cast<int>(slice / kFK));
@@ -457,7 +494,7 @@ static FfnGemm plan(int64_t rows, int64_t cols, int64_t K, int64_t slice, int ti
 
 bi_status launch_ffn_gate_up(Mat x, const __nv_bfloat16 *w13, __nv_bfloat16 *act, float *gu, int64_t M, int64_t H,
                              int64_t I, cudaStream_t s) {
-  FfnGemm p = plan(I, M, H, kSliceK, kFM, 32);
+  FfnGemm p = plan(I, M, H, kSliceK, kFM);
   p.out = act;
   p.ldo = I;
   p.gu = gu;
@@ -468,7 +505,7 @@ bi_status launch_ffn_gate_up(Mat x, const __nv_bfloat16 *w13, __nv_bfloat16 *act
 
 bi_status launch_ffn_down(const __nv_bfloat16 *act, const __nv_bfloat16 *w2, Mat addend, __nv_bfloat16 *out,
                           int64_t ldo, int64_t M, int64_t H, int64_t I, cudaStream_t s) {
-  FfnGemm p = plan(H, M, I, kSliceK, 2 * kFM, 32);
+  FfnGemm p = plan(H, M, I, kSliceK, 2 * kFM);
   p.out = out;
   p.ldo = ldo;
   p.addend = addend.p;
@@ -480,7 +517,7 @@ bi_status launch_ffn_down(const __nv_bfloat16 *act, const __nv_bfloat16 *w2, Mat
 
 bi_status launch_ffn_dact(Mat dout, const __nv_bfloat16 *w2, const float *gu, __nv_bfloat16 *dgu, int64_t M, int64_t H,
                           int64_t I, cudaStream_t s) {
-  FfnGemm p = plan(I, M, H, kSliceK, 2 * kFM, 32);
+  FfnGemm p = plan(I, M, H, kSliceK, 2 * kFM);
   p.out = dgu;
   p.ldo = 2 * I;
   p.gu = const_cast<float *>(gu);
@@ -492,7 +529,7 @@ bi_status launch_ffn_dact(Mat dout, const __nv_bfloat16 *w2, const float *gu, __
 
 bi_status launch_ffn_dx(const __nv_bfloat16 *dgu, const __nv_bfloat16 *w13, __nv_bfloat16 *dx, int64_t lddx, int64_t M,
                         int64_t H, int64_t I, cudaStream_t s) {
-  FfnGemm p = plan(H, M, 2 * I, kSliceK, 2 * kFM, 32);
+  FfnGemm p = plan(H, M, 2 * I, kSliceK, 2 * kFM);
   p.out = dx;
   p.ldo = lddx;
   CUtensorMap a, b;
@@ -502,7 +539,7 @@ bi_status launch_ffn_dx(const __nv_bfloat16 *dgu, const __nv_bfloat16 *w13, __nv
 
 bi_status launch_ffn_wgrad(Mat a, Mat b, void *dw, int grad_mode, int64_t M, int64_t rows, int64_t cols,
                            cudaStream_t s) {
-  FfnGemm p = plan(rows, cols, M, (M + kFK - 1) / kFK * kFK, 2 * kFM, 128);
+  FfnGemm p = plan(rows, cols, M, (M + kFK - 1) / kFK * kFK, 2 * kFM);
   p.out = dw;
   p.ldo = cols;
   p.mode = grad_mode;

@@ -34,57 +34,135 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
   return (c & 8u) ? -v : v;
 }
 
-// Byte of the scale of (row, block of 32) in the tiled scale array: tiles of
-// 128 rows x 4 blocks, 512 bytes each, in row-tile major order.
-__device__ __forceinline__ int64_t mx_scale_at(int64_t r, int64_t b, int64_t ktiles) {
-  return ((r / kMxTileRows) * ktiles + b / kMxTileScales) * kMxTileBytes + (r % 32) * 16 + (r / 32 % 4) * 4 +
-         b % kMxTileScales;
-}
-
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ void from_f32(float v, float &o) { o = v; }
-__device__ __forceinline__ void from_f32(float v, __nv_bfloat16 &o) { o = __float2bfloat16_rn(v); }
-
-// One thread per block of 32 values of the padded scale tiles: rows up to a
-// multiple of 128 and blocks up to a multiple of 4 get scale byte 0.
-template <typename T>
-__global__ void __launch_bounds__(256) mx4_quantize_kernel(const T *x, int64_t ldx, uint8_t *q, uint8_t *scales,
-                                                           int64_t R, int64_t K, int64_t rows_p, int64_t ktiles) {
-  griddep_wait();
-  const int64_t nb = ktiles * kMxTileScales;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= rows_p * nb) return;
-  const int64_t r = i / nb, b = i % nb;
-  uint8_t *sp = scales + mx_scale_at(r, b, ktiles);
-  if (r >= R || b >= K / kMxBlock) {
-    *sp = 0;
-    return;
-  }
-  const T *src = x + r * ldx + b * kMxBlock;
-  uint32_t amax = 0;
-  for (int j = 0; j < kMxBlock; ++j) amax = max(amax, __float_as_uint(to_f32(src[j])) & 0x7fffffffu);
-  const uint32_t e = amax >> 23;
-  const uint32_t s = e == 255 ? 255u : (e > 2 ? e - 2 : 0u);
-  *sp = static_cast<uint8_t>(s);
-  const float inv = __uint_as_float((254u - min(s, 253u)) << 23);
-  uint8_t *dst = q + r * (K / 2) + b * (kMxBlock / 2);
-  for (int j = 0; j < kMxBlock; j += 2) {
-    const float2 v = make_float2(to_f32(src[j]) * inv, to_f32(src[j + 1]) * inv);
-    dst[j / 2] = s == 255 ? 0 : static_cast<uint8_t>(__nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest));
+// Eight consecutive values in fp32.
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+  const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p));
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(u[j] << 16);
+    v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
   }
 }
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    u[j] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *(reinterpret_cast<float4 *>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// Quantisation and its inverse move bytes and little else.  One warp takes 256
+// consecutive values (8 per lane, a block per 4 lanes) of the rows r, r + 32,
+// r + 64 and r + 96 of a scale tile: their scale words are 16 consecutive bytes
+// of it, so scales move as 16-byte words too, and four rows' loads are in
+// flight per lane.
+constexpr int kQWarps = 8;
+constexpr int kQCols = 256;
+
+struct Mx4Task {
+  int64_t row, col;  // first row (of the four) and this lane's first value
+  int64_t sword;     // byte offset of the 16 scale bytes of this half warp
+};
+
+// Warp `w` of all: row tile, row within 32, 256-value chunk (fastest).
+__device__ __forceinline__ bool mx4_task(int64_t R, int64_t ktiles, int lane, Mx4Task &t) {
+  // (fewer than 2^32 warps: 2^32 * 1024 values exceed any memory)
+  const uint32_t w = blockIdx.x * kQWarps + (threadIdx.x >> 5);
+  const uint32_t chunks = static_cast<uint32_t>(ktiles + 1) / 2;
+  const uint32_t r = w / chunks, c = w % chunks;
+  if (r >= (R + kMxTileRows - 1) / kMxTileRows * 32) return false;
+  t.row = static_cast<int64_t>(r / 32) * kMxTileRows + r % 32;
+  t.col = c * kQCols + lane * 8;
+  t.sword = ((r / 32) * ktiles + 2 * c + lane / 16) * kMxTileBytes + r % 32 * 16;
+  return true;
+}
 
 template <typename T>
-__global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t *q, const uint8_t *scales, T *y, int64_t ldy,
-                                                             int64_t R, int64_t K, int64_t ktiles) {
+__global__ void __launch_bounds__(kQWarps * 32) mx4_quantize_kernel(const T *x, int64_t ldx, uint8_t *q,
+                                                                    uint8_t *scales, int64_t R, int64_t K,
+                                                                    int64_t ktiles) {
   griddep_wait();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= R * (K / 2)) return;
-  const int64_t r = i / (K / 2), j = i % (K / 2);
-  const float s = mx_scale(scales[mx_scale_at(r, j / 16, ktiles)]);
-  from_f32(e2m1_value(q[i] & 15u) * s, y[r * ldy + 2 * j]);
-  from_f32(e2m1_value(q[i] >> 4) * s, y[r * ldy + 2 * j + 1]);
+  const int lane = threadIdx.x & 31;
+  Mx4Task t;
+  if (!mx4_task(R, ktiles, lane, t)) return;
+  float v[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // rows past R and blocks past K hold zeros: scale byte 0
+    if (t.row + 32 * i < R && t.col < K) {
+      load8(x + (t.row + 32 * i) * ldx + t.col, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    }
+  }
+  uint32_t words[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[i][j]) & 0x7fffffffu);
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // the biased exponent of amax less E2M1's largest exponent
+    const uint32_t e = amax >> 23;
+    const uint32_t s = e == 255 ? 255u : (e > 2 ? e - 2 : 0u);
+    const float inv = __uint_as_float((254u - min(s, 253u)) << 23);
+    uint32_t code = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 p = make_float2(v[i][2 * j] * inv, v[i][2 * j + 1] * inv);
+      code |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(p, __NV_E2M1, cudaRoundNearest)) << (8 * j);
+    }
+    if (s == 255) code = 0;
+    if (t.row + 32 * i < R && t.col < K)
+      *reinterpret_cast<uint32_t *>(q + (t.row + 32 * i) * (K / 2) + t.col / 2) = code;
+    // the four scales of 128 values as one word on each of their 16 lanes
+    uint32_t w = s << (8 * ((lane >> 2) & 3));
+    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+    w |= __shfl_xor_sync(0xffffffffu, w, 8);
+    words[i] = w;
+  }
+  if ((lane & 15) == 0 && t.col / 128 < ktiles)
+    *reinterpret_cast<uint4 *>(scales + t.sword) = make_uint4(words[0], words[1], words[2], words[3]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kQWarps * 32) mx4_dequantize_kernel(const uint8_t *q, const uint8_t *scales, T *y,
+                                                                      int64_t ldy, int64_t R, int64_t K,
+                                                                      int64_t ktiles) {
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  Mx4Task t;
+  if (!mx4_task(R, ktiles, lane, t) || t.col >= K) return;
+  const uint4 w4 = *reinterpret_cast<const uint4 *>(scales + t.sword);
+  const uint32_t words[4] = {w4.x, w4.y, w4.z, w4.w};
+  uint32_t code[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    code[i] = t.row + 32 * i < R
+                  ? __ldcs(reinterpret_cast<const uint32_t *>(q + (t.row + 32 * i) * (K / 2) + t.col / 2))
+                  : 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (t.row + 32 * i >= R) break;
+    const float s = mx_scale((words[i] >> (8 * ((lane >> 2) & 3))) & 255u);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = e2m1_value((code[i] >> (4 * j)) & 15u) * s;
+    store8(y + (t.row + 32 * i) * ldy + t.col, v);
+  }
 }
 
 // ---------------------------------------------------------------- product --
@@ -356,27 +434,30 @@ __global__ void __launch_bounds__(kXThreads, 1)
   }
 }
 
-static unsigned blocks_of(int64_t n) { return static_cast<unsigned>((n + 255) / 256); }
+static dim3 quant_grid(int64_t R, int64_t K) {
+  const int64_t warps = (R + kMxTileRows - 1) / kMxTileRows * 32 * ((K + kQCols - 1) / kQCols);
+  return dim3(static_cast<unsigned>((warps + kQWarps - 1) / kQWarps));
+}
 
 bi_status launch_mx4_quantize(const void *x, bool f32, int64_t ldx, uint8_t *q, uint8_t *scales, int64_t R, int64_t K,
                               cudaStream_t s) {
-  const int64_t rows_p = (R + kMxTileRows - 1) / kMxTileRows * kMxTileRows, ktiles = (K + 127) / 128;
-  const dim3 grid(blocks_of(rows_p * ktiles * kMxTileScales));
+  const int64_t ktiles = (K + 127) / 128;
+  const dim3 block(kQWarps * 32);
   if (f32)
-    return launch_chained(mx4_quantize_kernel<float>, grid, dim3(256), 0, s, 1, static_cast<const float *>(x), ldx, q,
-                          scales, R, K, rows_p, ktiles);
-  return launch_chained(mx4_quantize_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1,
-                        static_cast<const __nv_bfloat16 *>(x), ldx, q, scales, R, K, rows_p, ktiles);
+    return launch_chained(mx4_quantize_kernel<float>, quant_grid(R, K), block, 0, s, 1, static_cast<const float *>(x),
+                          ldx, q, scales, R, K, ktiles);
+  return launch_chained(mx4_quantize_kernel<__nv_bfloat16>, quant_grid(R, K), block, 0, s, 1,
+                        static_cast<const __nv_bfloat16 *>(x), ldx, q, scales, R, K, ktiles);
 }
 
 bi_status launch_mx4_dequantize(const uint8_t *q, const uint8_t *scales, void *y, bool f32, int64_t ldy, int64_t R,
                                 int64_t K, cudaStream_t s) {
   const int64_t ktiles = (K + 127) / 128;
-  const dim3 grid(blocks_of(R * (K / 2)));
+  const dim3 block(kQWarps * 32);
   if (f32)
-    return launch_chained(mx4_dequantize_kernel<float>, grid, dim3(256), 0, s, 1, q, scales, static_cast<float *>(y),
-                          ldy, R, K, ktiles);
-  return launch_chained(mx4_dequantize_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, 1, q, scales,
+    return launch_chained(mx4_dequantize_kernel<float>, quant_grid(R, K), block, 0, s, 1, q, scales,
+                          static_cast<float *>(y), ldy, R, K, ktiles);
+  return launch_chained(mx4_dequantize_kernel<__nv_bfloat16>, quant_grid(R, K), block, 0, s, 1, q, scales,
                         static_cast<__nv_bfloat16 *>(y), ldy, R, K, ktiles);
 }
 
