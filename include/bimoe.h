@@ -717,6 +717,17 @@ BI_API bi_status bi_moe_gate_up_feed(int32_t mode, int32_t *previous);
 BI_API bi_status bi_moe_decode_fused(int32_t mode, int32_t *previous);
 
 /*
+ * bi_ffn_schedule -- which kernel runs the products of bi_ffn_forward,
+ * bi_ffn_forward_train and bi_ffn_backward that have tokens as columns, for
+ * the whole process from the next call on: 0 automatic (the default: by M),
+ * 1 always the CTA-pair kernel, 2 the split kernel (the reduction's slices
+ * over the CTAs of a cluster) wherever the reduction is at most 8192 long.
+ * Same bits either way (tests compare them).  *previous (may be NULL) receives
+ * the old setting; other values BI_ERR_INVALID_ARG.
+ */
+BI_API bi_status bi_ffn_schedule(int32_t mode, int32_t *previous);
+
+/*
  * bi_fp32_fma_probe -- MEASUREMENT ONLY, not part of the MoE path: blocks x
  * 256 threads, each running 16 independent fp32 FMA chains for `iters`
  * steps (2 * 16 * iters flop per thread, no memory traffic in the loop).

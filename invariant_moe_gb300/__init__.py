@@ -39,6 +39,7 @@ EXPORTS = [
     "bi_moe_gather_routing", "bi_moe_scatter_contrib", "bi_router_topk_bf16_schedule",
     "bi_moe_gate_up_tokens", "bi_moe_gate_up_feed", "bi_moe_layer", "bi_moe_decode_fused",
     "bi_ffn_workspace_bytes", "bi_ffn_forward", "bi_ffn_forward_train", "bi_ffn_backward",
+    "bi_ffn_schedule",
     "bi_mx4_scale_bytes", "bi_mx4_quantize", "bi_mx4_dequantize", "bi_mx4_gemm", "bi_mx4_gate_up",
 ]
 
@@ -105,6 +106,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "bi_ffn_forward": ([P, I64, P, P, P, I64, P, I64, I64, I64, I64, P, SZ, P], ST),
             "bi_ffn_forward_train": ([P, I64, P, P, P, I64, P, I64, P, P, I64, I64, I64, P], ST),
             "bi_ffn_backward": ([P, I64, P, I64, P, P, P, P, P, I64, P, P, I32, I64, I64, I64, P, SZ, P], ST),
+            "bi_ffn_schedule": ([I32, P], ST),
             "bi_mx4_scale_bytes": ([I64, I64], SZ),
             "bi_mx4_quantize": ([P, I32, I64, P, P, I64, I64, P], ST),
             "bi_mx4_dequantize": ([P, P, P, I32, I64, I64, I64, P], ST),
@@ -674,6 +676,14 @@ def bi_ffn_backward(dout, x, w13, w2, gu, act, dx=None, dw13=None, dw2=None, nee
             _flat(gu, _F32, "gu", dev), _flat(act, _BF, "act", dev), pdx, lddx, p13, p2, mode, M, H, I,
             _flat(workspace, _U8, "workspace", dev), workspace.numel())
     return dx if need[0] else None, dw13 if need[1] else None, dw2 if need[2] else None
+
+
+def bi_ffn_schedule(mode):
+    """Which kernel runs the feed-forward products over tokens (0 automatic, 1 CTA pairs, 2 slices over a
+    cluster); returns the previous setting."""
+    prev = ctypes.c_int32(0)
+    _call("bi_ffn_schedule", int(mode), ctypes.byref(prev))
+    return prev.value
 
 
 # ------------------------------------ microscaled 4-bit floating point --

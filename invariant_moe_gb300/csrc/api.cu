@@ -246,7 +246,8 @@ bool make_tma_2d_u8(CUtensorMap *map, const void *base, uint64_t rows, uint64_t 
   return true;
 }
 
-bool make_tma_inter_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t I, uint64_t K) {
+bool make_tma_inter_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t I, uint64_t K,
+                         uint32_t groups) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) {
     set_error("cuTensorMapEncodeTiled is not available from the driver");
@@ -258,7 +259,7 @@ bool make_tma_inter_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint
   }
   const cuuint64_t dims[4] = {K, 16, 2, rows / 16};
   const cuuint64_t strides[3] = {K * 2, I * K * 2, 16 * K * 2};
-  const cuuint32_t box[4] = {64, 16, 2, 4};
+  const cuuint32_t box[4] = {64, 16, 2, groups};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
                         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -884,6 +885,13 @@ BI_API bi_status bi_ffn_backward(const bi_bf16 *dout, int64_t lddo, const bi_bf1
   if (dw2) BI_TRY(launch_ffn_wgrad(mat(dout, lddo), mat(act, I), dw2, grad_mode, M, H, I, s));
   if (dx) BI_TRY(launch_ffn_dx(dgu, cbf(w13), mbf(dx), lddx, M, H, I, s));
   if (dw13) BI_TRY(launch_ffn_wgrad(Mat{dgu, 2 * I}, mat(x, ldx), dw13, grad_mode, M, 2 * I, H, s));
+  return BI_OK;
+}
+
+BI_API bi_status bi_ffn_schedule(int32_t mode, int32_t *previous) {
+  BI_REQUIRE(mode >= 0 && mode <= 2, BI_ERR_INVALID_ARG, "feed-forward schedule %d not in {0, 1, 2}", mode);
+  const int old = bimoe::set_ffn_schedule(mode);
+  if (previous) *previous = old;
   return BI_OK;
 }
 

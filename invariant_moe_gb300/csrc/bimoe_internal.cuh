@@ -51,7 +51,9 @@ bool make_tma_2d_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_
 // a box {64, 16, 2, 4} at group g lands 16 gate rows, the 16 up rows of the
 // same features (I rows further), and so on for four groups: 64 features'
 // interleaved rows in one copy, 128-byte swizzled like the 2-D map's.
-bool make_tma_inter_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t I, uint64_t K);
+// (`groups` 16-row gate/up pairs per copy, four unless said otherwise.)
+bool make_tma_inter_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t I, uint64_t K,
+                         uint32_t groups = 4);
 // Encode a 2-D bf16 TMA map over [rows, cols] with row stride ld (elements) and
 // a [box_rows, 64]-element box, 128-byte swizzle.
 bool make_tma_2d_bf16_ld(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld,
@@ -329,6 +331,12 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
+}
+// fp32 load from the shared memory of a CTA of the cluster (cluster address).
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
 }
 // Arrive on an mbarrier given by its cluster address (own or peer CTA).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {

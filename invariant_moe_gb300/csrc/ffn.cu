@@ -27,6 +27,7 @@
 //     registers, so tensor memory is free again before anything is stored.
 //     gate/up: each CTA holds 64 gate rows and the matching 64 up rows in
 //     16-row groups, so a lane and lane ^ 16 hold both projections of a feature.
+#include <atomic>
 #include <mutex>
 
 #include "ffn_internal.cuh"
@@ -68,6 +69,14 @@ struct FfnGemm {
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return __fmul_rn(__fdividef(g, __fadd_rn(1.0f, __expf(-g))), u);
 }
+
+// The two projections' gradients from dact = d: one fixed fp32 sequence.
+__device__ __forceinline__ float gate_sigmoid(float g) { return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-g))); }
+__device__ __forceinline__ float dgate(float d, float g, float u) {
+  const float s = gate_sigmoid(g);
+  return __fmul_rn(__fmul_rn(__fmul_rn(d, u), s), __fmaf_rn(g, __fsub_rn(1.0f, s), 1.0f));
+}
+__device__ __forceinline__ float dup(float d, float g) { return __fmul_rn(__fmul_rn(d, g), gate_sigmoid(g)); }
 
 // 32 bytes to global memory: a whole sector per lane.
 __device__ __forceinline__ void store_32b(void *p, const uint32_t (&v)[8], bool wide) {
@@ -167,11 +176,10 @@ __device__ __forceinline__ void ffn_epilogue(const FfnGemm &p, const float (&acc
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const float gv = g[(c / 16) & 1][j], uv = u[(c / 16) & 1][j];
-        const float s = __fdividef(1.0f, __fadd_rn(1.0f, __expf(-gv)));
         const float d = acc[c + j];
         if (c + j < limit) {
-          o[(c + j) * two] = __float2bfloat16_rn(d * uv * s * (1.0f + gv * (1.0f - s)));
-          o[(c + j) * two + p.rows] = __float2bfloat16_rn(d * gv * s);
+          o[(c + j) * two] = __float2bfloat16_rn(dgate(d, gv, uv));
+          o[(c + j) * two + p.rows] = __float2bfloat16_rn(dup(d, gv));
         }
       }
     }
@@ -416,6 +424,215 @@ __global__ void __launch_bounds__(kFThreads, 1)
   }
 }
 
+// ------------------------------------------------- few tokens: split kernel --
+//
+// With few tokens the weights are the whole cost and the pair tiles above are
+// too few to stream them.  Here every slice of a row tile has a CTA of its own:
+// the CTAs of a cluster take one slice each (same K=16 chains into tensor
+// memory), leave their partial tiles in shared memory and, after a cluster
+// barrier, add them through distributed shared memory in slice order from +0 --
+// the recipe of the pair kernel, so the bits are the same.
+//   * A row tile is 128, 64 or 32 rows (the MMA still takes 128: the rest reads
+//     whatever shared memory holds, in accumulator rows that nothing reads), so
+//     that there are about as many CTAs as SMs.
+//   * All of a slice's stages are in flight at once where they fit; up to 64
+//     tokens a CTA keeps to half of an SM's shared memory, so that the down
+//     kernel's CTAs start beside the gate/up ones and load W2 (which no kernel
+//     between writes) while those still run.
+constexpr int kPThreads = 192;      // TMA, MMA, 4 epilogue warps
+constexpr int kPMaxSlices = 8;      // CTAs of a cluster
+constexpr int kPMaxStages = 16;     // a slice's K steps
+
+struct FfnSplit {
+  FfnGemm g;
+  int tile_rows;          // rows of A per tile
+  int stages, stage_bytes, b_off;
+  int early;              // A may be read before the predecessor has finished
+};
+
+// One finished element of the result: D[row, col] (gate/up: the gate value and
+// `up` of feature `row`).
+template <FfnEpi EPI>
+__device__ __forceinline__ void ffn_store_one(const FfnGemm &p, int f, int t, float d, float up) {
+  if constexpr (EPI == kGateUp) {
+    static_cast<__nv_bfloat16 *>(p.out)[t * p.ldo + f] = __float2bfloat16_rn(silu_mul(d, up));
+    if (p.gu) {
+      float *gu = p.gu + static_cast<int64_t>(t) * 2 * p.rows + f;
+      gu[0] = d;
+      gu[p.rows] = up;
+    }
+  } else if constexpr (EPI == kStore) {
+    if (p.addend) d = __fadd_rn(d, __bfloat162float(p.addend[t * p.ld_add + f]));
+    static_cast<__nv_bfloat16 *>(p.out)[t * p.ldo + f] = __float2bfloat16_rn(d);
+  } else {
+    const int64_t at = static_cast<int64_t>(t) * 2 * p.rows + f;
+    const float g = p.gu[at], u = p.gu[at + p.rows];
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + at;
+    o[0] = __float2bfloat16_rn(dgate(d, g, u));
+    o[p.rows] = __float2bfloat16_rn(dup(d, g));
+  }
+}
+
+template <FfnEpi EPI, bool A_MN>
+__global__ void __launch_bounds__(kPThreads)
+    ffn_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ FfnSplit sp) {
+  const FfnGemm &prm = sp.g;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *aux = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(aux);
+  uint64_t *empty = full + kPMaxStages;
+  uint64_t *done = empty + kPMaxStages;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  uint8_t *tiles = aux + 1024;
+  float *part = reinterpret_cast<float *>(tiles);  // [n][tile_rows], over the stages once the MMAs are done
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slices = (prm.nkb + prm.slice_kb - 1) / prm.slice_kb;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int row = static_cast<int>(blockIdx.x) / slices * sp.tile_rows;  // first row of A (interleaved rows)
+  const int col = static_cast<int>(blockIdx.y) * prm.n;
+  const int kb0 = rank * prm.slice_kb, kb1 = min(prm.nkb, kb0 + prm.slice_kb);
+  uint32_t tmem_cols = 32;
+  while (tmem_cols < static_cast<uint32_t>(prm.n)) tmem_cols *= 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < sp.stages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(done), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 0) {
+    // ---------------------------------------------------- TMA producer --
+    if (elect_one()) {
+      auto load_a = [&](int i) {  // K step i of this slice
+        const int s = i % sp.stages, k = (kb0 + i) * kFK;
+        const uint32_t st = smem_u32(tiles + s * sp.stage_bytes), fb = smem_u32(&full[s]);
+        mbar_arrive_expect_tx(fb, static_cast<uint32_t>((sp.tile_rows + prm.n) * kFK * 2));
+        if (EPI == kGateUp) {
+          tma_load_4d(st, &tmA, fb, k, 0, 0, row / 32);
+        } else if (A_MN) {
+          for (int m = 0; m < sp.tile_rows; m += 64) tma_load_2d(st + m / 64 * kFSlab, &tmA, fb, row + m, k);
+        } else {
+          tma_load_2d(st, &tmA, fb, k, row);
+        }
+      };
+      const int steps = kb1 - kb0;
+      const int early = sp.early ? min(sp.stages, steps) : 0;
+      for (int i = 0; i < early; ++i) load_a(i);
+      griddep_wait();
+      int issued = early;  // steps whose stage is armed
+      for (int i = 0; i < steps; ++i) {
+        const int s = i % sp.stages;
+        if (i >= early) {
+          if (!mbar_wait(smem_u32(&empty[s]), (i / sp.stages & 1) ^ 1, abort_flag, prm.err)) break;
+          load_a(i);
+          issued = i + 1;
+        }
+        tma_load_2d(smem_u32(tiles + s * sp.stage_bytes + sp.b_off), &tmB, smem_u32(&full[s]), (kb0 + i) * kFK, col);
+      }
+      if (*abort_flag) {  // every copy this CTA started lands before it exits
+        for (int i = max(0, issued - sp.stages); i < issued; ++i)
+          mbar_wait(smem_u32(&full[i % sp.stages]), i / sp.stages & 1, nullptr, prm.err);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------ MMA issuer --
+    if (elect_one()) {
+      const uint32_t idesc = idesc_bf16_f32(kFM, prm.n) | (A_MN ? kIdescAMn : 0u);
+      for (int i = 0; i < kb1 - kb0; ++i) {
+        const int s = i % sp.stages;
+        if (!mbar_wait(smem_u32(&full[s]), i / sp.stages & 1, abort_flag, prm.err)) break;
+        tc_fence_after();
+        const uint32_t a0 = smem_u32(tiles + s * sp.stage_bytes), b0 = a0 + sp.b_off;
+#pragma unroll
+        for (int k = 0; k < kFK / 16; ++k)
+          umma_f16(tmem_base, A_MN ? sdesc_sw128_mn(a0 + k * 2048, kFSlab) : sdesc_sw128(a0 + k * 32),
+                   sdesc_sw128(b0 + k * 32), idesc, (i | k) ? 1u : 0u);
+        umma_commit(smem_u32(&empty[s]));
+      }
+      umma_commit(smem_u32(done));
+    }
+    __syncwarp();
+  }
+  griddep_wait();
+  // the dependent kernel may start: everything before this one has finished
+  griddep_launch_dependents();
+  // ---------------------------------------------------------- epilogue --
+  // (also after an abort: the MMAs that were issued complete)
+  const bool ok = __syncthreads_and(mbar_wait(smem_u32(done), 0, nullptr, prm.err) && !*abort_flag) != 0;
+  tc_fence_after();
+  if (warp >= 2 && ok) {
+    const int q = warp & 3;
+    if (q * 32 < sp.tile_rows) {
+      const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+      for (int c = 0; c < prm.n; c += 16) {
+        uint32_t d[16];
+        tmem_ld16(t + c, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * sp.tile_rows + q * 32 + lane] = __uint_as_float(d[j]);
+      }
+    }
+  }
+  tc_fence_before();
+  if (slices > 1) cluster_sync_all();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, tmem_cols);
+  }
+  if (ok) {
+    // this CTA's share of the tile's elements, features fastest
+    const int feats = EPI == kGateUp ? sp.tile_rows / 2 : sp.tile_rows;
+    const int f0 = EPI == kGateUp ? row / 2 : row;
+    const int items = feats * min(prm.n, prm.cols - col);
+    const int per = (items + slices * 32 - 1) / (slices * 32) * 32;
+    const int end = min(items, (rank + 1) * per);
+    uint32_t base[kPMaxSlices];
+#pragma unroll
+    for (int s = 0; s < kPMaxSlices; ++s) base[s] = s < slices ? mapa_shared(smem_u32(part), s) : 0u;
+    for (int i = rank * per + static_cast<int>(threadIdx.x); i < end; i += kPThreads) {
+      const int f = i % feats, c = i / feats;
+      const int r = EPI == kGateUp ? f / 16 * 32 + f % 16 : f;
+      const uint32_t at = static_cast<uint32_t>((c * sp.tile_rows + r) * 4);
+      float v[kPMaxSlices], w[kPMaxSlices];
+#pragma unroll
+      for (int s = 0; s < kPMaxSlices; ++s)
+        if (s < slices) {
+          v[s] = ld_cluster_f32(base[s] + at);
+          if (EPI == kGateUp) w[s] = ld_cluster_f32(base[s] + at + 64);
+        }
+      float d = 0.0f, up = 0.0f;
+#pragma unroll
+      for (int s = 0; s < kPMaxSlices; ++s)
+        if (s < slices) {
+          d = __fadd_rn(d, v[s]);
+          if (EPI == kGateUp) up = __fadd_rn(up, w[s]);
+        }
+      if (f0 + f < prm.rows) ffn_store_one<EPI>(prm, f0 + f, col + c, d, up);
+    }
+  }
+  if (slices > 1) cluster_sync_all();  // no CTA leaves while another reads its partials
+}
+
 // ------------------------------------------------------------------- host --
 template <FfnEpi EPI, bool A_MN, bool B_MN>
 static bi_status launch_ffn(const CUtensorMap &tmA, const CUtensorMap &tmB, FfnGemm p, cudaStream_t s) {
@@ -470,15 +687,17 @@ static int div_up(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / 
 // tile: the multiple of 32 up to 256 with the least time by a simple model:
 // waves of tiles over the CTA pairs, each as long as its columns plus a
 // constant (what a tile costs besides its MMAs, and that narrow MMAs do not
-// run faster than about 64 columns' time).
-static FfnGemm plan(int64_t rows, int64_t cols, int64_t K, int64_t slice, int tile_rows) {
+// run faster than about 64 columns' time).  MN-major B (n_step 128): only whole
+// slabs per CTA, as a part of a slab costs a whole one's copy (dW2 of 8191
+// tokens, H=4096, I=2048: 104 us with 160 columns, 85 us with 256).
+static FfnGemm plan(int64_t rows, int64_t cols, int64_t K, int64_t slice, int tile_rows, int n_step) {
   FfnGemm p{};
   p.rows = static_cast<int>(rows);
   p.cols = static_cast<int>(cols);
   p.m_tiles = div_up(rows, tile_rows);
   const int64_t pairs = std::max(1, num_sms() / 2);
   int64_t best = INT64_MAX;
-  for (int n = 256; n >= 32; n -= 32) {
+  for (int n = 256; n >= n_step; n -= n_step) {
     const int64_t tiles = static_cast<int64_t>(p.m_tiles) * div_up(cols, n);
     const int64_t cost = (tiles + pairs - 1) / pairs * (std::max(n, 64) + 16);
     if (cost < best) {
@@ -492,12 +711,80 @@ static FfnGemm plan(int64_t rows, int64_t cols, int64_t K, int64_t slice, int ti
   return p;
 }
 
+// 0: automatic, 1: always the pair kernel, 2: the split kernel wherever the
+// reduction has at most kPMaxSlices slices.
+static std::atomic<int> g_ffn_schedule{0};
+
+int set_ffn_schedule(int mode) { return g_ffn_schedule.exchange(mode); }
+
+static bool use_split(int64_t M, int64_t K) {
+  const int mode = g_ffn_schedule.load();
+  return mode != 1 && (K + kSliceK - 1) / kSliceK <= kPMaxSlices && (mode == 2 || M <= 256);
+}
+
+// The split kernel over `rows` rows of A (gate/up: 2I interleaved ones) and M
+// tokens.  map_a encodes A's tensor map for a given tile height.
+template <FfnEpi EPI, bool A_MN, typename MapA>
+static bi_status launch_split(FfnGemm g, int64_t rows, int64_t M, int64_t K, bool early, MapA map_a,
+                              const void *tokens, int64_t ld_tokens, cudaStream_t s) {
+  FfnSplit p{};
+  g.nkb = div_up(K, kFK);
+  g.slice_kb = kSliceK / kFK;
+  g.cols = static_cast<int>(M);
+  g.n = static_cast<int>(std::min<int64_t>(256, (M + 15) / 16 * 16));
+  g.err = device_error_word();
+  p.g = g;
+  const int slices = div_up(K, kSliceK), token_tiles = div_up(M, g.n);
+  // the tallest tiles that still give four fifths of the SMs a CTA
+  p.tile_rows = kFM;
+  while (p.tile_rows > (A_MN ? 64 : 32) &&
+         static_cast<int64_t>(div_up(rows, p.tile_rows)) * slices * token_tiles * 5 < num_sms() * 4)
+    p.tile_rows /= 2;
+  p.b_off = p.tile_rows * kFK * 2;
+  p.stage_bytes = p.b_off + g.n * kFK * 2;
+  p.early = early;
+  // the MMA reads 128 rows (16 KB) from every stage's start
+  const int limit = g.n <= 64 ? 112 * 1024 : 227 * 1024;
+  p.stages = std::min({kPMaxStages, std::min(g.nkb, g.slice_kb), (limit - 2048 - kFABytes) / p.stage_bytes});
+  const int partial = g.n * p.tile_rows * 4;
+  const int smem = 2048 + std::max(p.stages * p.stage_bytes + kFABytes, partial);
+  if (token_tiles > 65535) {
+    set_error("feed-forward product with %d token tiles", token_tiles);
+    return BI_ERR_UNSUPPORTED;
+  }
+  static std::mutex mu;
+  static ContextSetup setup;  // the shared-memory attribute is per context
+  int dev = 0;
+  cudaGetDevice(&dev);
+  auto kern = ffn_split_kernel<EPI, A_MN>;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (setup.pending(dev)) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+      if (e != cudaSuccess) {
+        cudaGetLastError();
+        set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        return BI_ERR_CUDA;
+      }
+      setup.done(dev);
+    }
+  }
+  CUtensorMap a, b;
+  if (!map_a(&a, p.tile_rows) || !make_tma_2d_bf16_ld(&b, tokens, M, K, ld_tokens, g.n)) return BI_ERR_CUDA;
+  return launch_chained(kern, dim3(div_up(rows, p.tile_rows) * slices, token_tiles), dim3(kPThreads), smem, s, slices,
+                        a, b, p);
+}
+
 bi_status launch_ffn_gate_up(Mat x, const __nv_bfloat16 *w13, __nv_bfloat16 *act, float *gu, int64_t M, int64_t H,
                              int64_t I, cudaStream_t s) {
-  FfnGemm p = plan(I, M, H, kSliceK, kFM);
+  FfnGemm p = plan(I, M, H, kSliceK, kFM, 32);
   p.out = act;
   p.ldo = I;
   p.gu = gu;
+  if (use_split(M, H))
+    return launch_split<kGateUp, false>(
+        p, 2 * I, M, H, false,
+        [&](CUtensorMap *a, int r) { return make_tma_inter_bf16(a, w13, I, I, H, r / 32); }, x.p, x.ld, s);
   CUtensorMap a, b;
   if (!make_tma_inter_bf16(&a, w13, I, I, H) || !make_tma_2d_bf16_ld(&b, x.p, M, H, x.ld, p.n / 2)) return BI_ERR_CUDA;
   return launch_ffn<kGateUp, false, false>(a, b, p, s);
@@ -505,11 +792,14 @@ bi_status launch_ffn_gate_up(Mat x, const __nv_bfloat16 *w13, __nv_bfloat16 *act
 
 bi_status launch_ffn_down(const __nv_bfloat16 *act, const __nv_bfloat16 *w2, Mat addend, __nv_bfloat16 *out,
                           int64_t ldo, int64_t M, int64_t H, int64_t I, cudaStream_t s) {
-  FfnGemm p = plan(H, M, I, kSliceK, 2 * kFM);
+  FfnGemm p = plan(H, M, I, kSliceK, 2 * kFM, 32);
   p.out = out;
   p.ldo = ldo;
   p.addend = addend.p;
   p.ld_add = addend.ld;
+  if (use_split(M, I))  // launched behind launch_ffn_gate_up, which writes no weights: W2 may be read early
+    return launch_split<kStore, false>(
+        p, H, M, I, true, [&](CUtensorMap *a, int r) { return make_tma_2d_bf16(a, w2, H, I, r); }, act, I, s);
   CUtensorMap a, b;
   if (!make_tma_2d_bf16(&a, w2, H, I, kFM) || !make_tma_2d_bf16(&b, act, M, I, p.n / 2)) return BI_ERR_CUDA;
   return launch_ffn<kStore, false, false>(a, b, p, s);
@@ -517,10 +807,13 @@ bi_status launch_ffn_down(const __nv_bfloat16 *act, const __nv_bfloat16 *w2, Mat
 
 bi_status launch_ffn_dact(Mat dout, const __nv_bfloat16 *w2, const float *gu, __nv_bfloat16 *dgu, int64_t M, int64_t H,
                           int64_t I, cudaStream_t s) {
-  FfnGemm p = plan(I, M, H, kSliceK, 2 * kFM);
+  FfnGemm p = plan(I, M, H, kSliceK, 2 * kFM, 32);
   p.out = dgu;
   p.ldo = 2 * I;
   p.gu = const_cast<float *>(gu);
+  if (use_split(M, H))
+    return launch_split<kDact, true>(
+        p, I, M, H, false, [&](CUtensorMap *a, int) { return make_tma_2d_bf16(a, w2, H, I, kFK); }, dout.p, dout.ld, s);
   CUtensorMap a, b;
   if (!make_tma_2d_bf16(&a, w2, H, I, kFK) || !make_tma_2d_bf16_ld(&b, dout.p, M, H, dout.ld, p.n / 2))
     return BI_ERR_CUDA;
@@ -529,9 +822,13 @@ bi_status launch_ffn_dact(Mat dout, const __nv_bfloat16 *w2, const float *gu, __
 
 bi_status launch_ffn_dx(const __nv_bfloat16 *dgu, const __nv_bfloat16 *w13, __nv_bfloat16 *dx, int64_t lddx, int64_t M,
                         int64_t H, int64_t I, cudaStream_t s) {
-  FfnGemm p = plan(H, M, 2 * I, kSliceK, 2 * kFM);
+  FfnGemm p = plan(H, M, 2 * I, kSliceK, 2 * kFM, 32);
   p.out = dx;
   p.ldo = lddx;
+  if (use_split(M, 2 * I))
+    return launch_split<kStore, true>(
+        p, H, M, 2 * I, false, [&](CUtensorMap *a, int) { return make_tma_2d_bf16(a, w13, 2 * I, H, kFK); }, dgu, 2 * I,
+        s);
   CUtensorMap a, b;
   if (!make_tma_2d_bf16(&a, w13, 2 * I, H, kFK) || !make_tma_2d_bf16(&b, dgu, M, 2 * I, p.n / 2)) return BI_ERR_CUDA;
   return launch_ffn<kStore, true, false>(a, b, p, s);
@@ -539,7 +836,7 @@ bi_status launch_ffn_dx(const __nv_bfloat16 *dgu, const __nv_bfloat16 *w13, __nv
 
 bi_status launch_ffn_wgrad(Mat a, Mat b, void *dw, int grad_mode, int64_t M, int64_t rows, int64_t cols,
                            cudaStream_t s) {
-  FfnGemm p = plan(rows, cols, M, (M + kFK - 1) / kFK * kFK, 2 * kFM);
+  FfnGemm p = plan(rows, cols, M, (M + kFK - 1) / kFK * kFK, 2 * kFM, 128);
   p.out = dw;
   p.ldo = cols;
   p.mode = grad_mode;

@@ -31,6 +31,8 @@ bi_status launch_ffn_dx(const __nv_bfloat16 *dgu, const __nv_bfloat16 *w13, __nv
 bi_status launch_ffn_wgrad(Mat a, Mat b, void *dw, int grad_mode, int64_t M, int64_t rows, int64_t cols,
                            cudaStream_t s);
 
+int set_ffn_schedule(int mode);  // bi_ffn_schedule; returns the old mode
+
 constexpr int kMxBlock = 32;       // values that share a scale
 constexpr int kMxTileRows = 128;   // a scale tile: 128 rows x 4 scales, 512 bytes
 constexpr int kMxTileScales = 4;

@@ -298,3 +298,23 @@ def test_refusals(cuda):
         bm.bi_ffn_backward(dout, x, w13, w2, gu, act, dw13=w13.half(), dw2=w2.half())
     with pytest.raises(TypeError):  # one gradient bf16, the other fp32
         bm.bi_ffn_backward(dout, x, w13, w2, gu, act, dw13=w13.clone(), dw2=w2.float())
+
+
+@pytest.mark.parametrize("M,H,I", [(1, 4096, 2048), (5, 1040, 336), (64, 2048, 768), (200, 3088, 1056),
+                                   (256, 8192, 64), (300, 512, 528), (700, 2048, 16)])
+def test_schedules_agree(cuda, M, H, I):
+    """The CTA-pair kernel and the split kernel give the same bits, forward and backward."""
+    import invariant_moe_gb300 as bm
+    x, w13, w2, add, dout = (t.to(cuda) for t in make(M, H, I, 120))
+    got = []
+    old = bm.bi_ffn_schedule(0)
+    try:
+        for mode in (1, 2):
+            bm.bi_ffn_schedule(mode)
+            out, gu, act = bm.bi_ffn_forward_train(x, w13, w2, addend=add)
+            got.append((bm.bi_ffn_forward(x, w13, w2, addend=add), out, gu, act,
+                        bm.bi_ffn_backward(dout, x, w13, w2, gu, act, need=(True, False, False))[0]))
+    finally:
+        bm.bi_ffn_schedule(old)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
