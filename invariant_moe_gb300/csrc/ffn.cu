@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
-  if (warp == 1) {
+  if (warp == 2) {
     if (lane == 0) *tmem_slot = 0u;
     __syncwarp();
     tmem_alloc_pair(smem_u32(tmem_slot), 2 * kFAccCols);
@@ -266,6 +266,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFRegsFew));
+    // The TMA and the MMA thread are alone in their warps: while other lanes
+    // wait for it at a warp or block barrier, every branch of a single lane
+    // takes some 70 cycles and a wait on an mbarrier 280 instead of 46
+    // (four M=128 x N=16 MMAs with a wait: 288 cycles, alone 194).
     if (warp == 0) {
       // ---------------------------------------------------- TMA producer --
       if (elect_one()) {
@@ -319,8 +323,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
           while (globaltimer_ns() - t0 < 200000ull) {
           }
         }
+      } else {
+        return;
       }
-      __syncwarp();
     } else if (warp == 1) {
       // ------------------------------------------------------ MMA issuer --
       if (rank == 0 && elect_one()) {
@@ -367,8 +372,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
         // every MMA into both CTAs' tensor memory has completed
         umma_commit_pair(smem_u32(drain), 0x3);
         wait(smem_u32(drain), 0, nullptr);
+      } else {
+        return;
       }
-      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFRegsMany));
@@ -383,7 +389,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
       for (int kb0 = 0; kb0 < prm.nkb; kb0 += prm.slice_kb) {
-        ok = __all_sync(0xffffffffu, wait(smem_u32(&tfull[buf]), buf_phase, abort_flag) ? 1 : 0) != 0;
+        // one lane polls: 256 polling threads slow the MMA thread's own waits
+        int landed = 1;
+        if (lane == 0) landed = wait(smem_u32(&tfull[buf]), buf_phase, abort_flag) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, landed, 0) != 0;
         if (!ok) break;
         tc_fence_after();
         const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
@@ -416,9 +425,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
   tc_fence_before();
   __syncthreads();
   // the even CTA's final commit: its last MMAs have left this CTA's memory too
-  if (rank != 0 && threadIdx.x == 32) wait(smem_u32(drain), 0, nullptr);
-  cluster_sync_all();  // neither CTA leaves while the other may still signal its barriers
-  if (warp == 1) {
+  if (rank != 0 && threadIdx.x == 96) wait(smem_u32(drain), 0, nullptr);
+  cluster_sync_rest();  // neither CTA leaves while the other may still signal its barriers
+  if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, 2 * kFAccCols);
   }
@@ -430,23 +439,33 @@ __global__ void __launch_bounds__(kFThreads, 1)
 // too few to stream them.  Here every slice of a row tile has a CTA of its own:
 // the CTAs of a cluster take one slice each (same K=16 chains into tensor
 // memory), leave their partial tiles in shared memory and, after a cluster
-// barrier, add them through distributed shared memory in slice order from +0 --
-// the recipe of the pair kernel, so the bits are the same.
-//   * A row tile is 128, 64 or 32 rows (the MMA still takes 128: the rest reads
-//     whatever shared memory holds, in accumulator rows that nothing reads), so
-//     that there are about as many CTAs as SMs.
-//   * All of a slice's stages are in flight at once where they fit; up to 64
-//     tokens a CTA keeps to half of an SM's shared memory, so that the down
-//     kernel's CTAs start beside the gate/up ones and load W2 (which no kernel
-//     between writes) while those still run.
-constexpr int kPThreads = 192;      // TMA, MMA, 4 epilogue warps
+// barrier, each adds its share of the elements through distributed shared
+// memory in slice order from +0 -- the recipe of the pair kernel, so the bits
+// are the same.  (Sending the partials instead, one 32-bit store each, took
+// 5 us for 32 rows x 48 tokens; reading them takes 0.7 us.)
+//   * A row tile is 128, 64 or 32 rows, so that there are about as many CTAs as
+//     SMs; up to 64 rows the MMA is an M=64 one (24 cycles each at N=16
+//     instead of 40).  Rows past the tile's read whatever shared memory holds,
+//     in accumulator rows that nothing reads.
+//   * A CTA keeps to half of an SM's shared memory, so that the down kernel's
+//     CTAs start beside the gate/up ones and load W2 (which no kernel between
+//     writes) while those still run.
+//   * Weights and tokens have a TMA thread each: one thread takes some 300
+//     cycles to arm a stage and issue both copies, longer than a K step's MMAs.
+//     A stage is two K steps, so that the MMA thread waits half as often.
+constexpr int kPThreads = 224;      // weight TMA, MMA, token TMA, 4 epilogue warps
 constexpr int kPMaxSlices = 8;      // CTAs of a cluster
-constexpr int kPMaxStages = 16;     // a slice's K steps
+constexpr int kPK = 2 * kFK;        // reduction step of a stage
+constexpr int kPMaxStages = kSliceK / kPK;
+constexpr int kPMaxN = 64;          // tokens per tile
+constexpr int kPSmem = 112 * 1024;
 
 struct FfnSplit {
   FfnGemm g;
   int tile_rows;          // rows of A per tile
+  int mma_rows;           // M of the MMA: 128, or 64 for tiles of up to 64 rows
   int stages, stage_bytes, b_off;
+  int share;              // elements that a CTA of the cluster finishes
   int early;              // A may be read before the predecessor has finished
 };
 
@@ -477,6 +496,7 @@ template <FfnEpi EPI, bool A_MN>
 __global__ void __launch_bounds__(kPThreads)
     ffn_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ FfnSplit sp) {
+  constexpr int kHalves = EPI == kGateUp ? 2 : 1;  // accumulators of an element: gate and up, or one
   const FfnGemm &prm = sp.g;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *aux = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -487,21 +507,22 @@ __global__ void __launch_bounds__(kPThreads)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   uint8_t *tiles = aux + 1024;
-  float *part = reinterpret_cast<float *>(tiles);  // [n][tile_rows], over the stages once the MMAs are done
+  float *part = reinterpret_cast<float *>(tiles);  // [token][tile_rows], over the stages once the MMAs are done
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slices = (prm.nkb + prm.slice_kb - 1) / prm.slice_kb;
   const int rank = static_cast<int>(cluster_ctarank());
   const int row = static_cast<int>(blockIdx.x) / slices * sp.tile_rows;  // first row of A (interleaved rows)
   const int col = static_cast<int>(blockIdx.y) * prm.n;
-  const int kb0 = rank * prm.slice_kb, kb1 = min(prm.nkb, kb0 + prm.slice_kb);
-  uint32_t tmem_cols = 32;
-  while (tmem_cols < static_cast<uint32_t>(prm.n)) tmem_cols *= 2;
+  const int k0 = rank * kSliceK;
+  const int steps = (min(prm.nkb - rank * prm.slice_kb, prm.slice_kb) + 1) / 2;  // stages of this slice
+  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), tiles0 = smem_u32(tiles);
+  const uint32_t tmem_cols = prm.n <= 32 ? 32 : 64;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < sp.stages; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(full0 + s * 8, 1);
+      mbar_init(empty0 + s * 8, 1);
     }
     mbar_init(smem_u32(done), 1);
     *abort_flag = 0;
@@ -509,7 +530,7 @@ __global__ void __launch_bounds__(kPThreads)
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
-  if (warp == 1) {
+  if (warp == 3) {
     tmem_alloc(smem_u32(tmem_slot), tmem_cols);
     tmem_relinquish();
   }
@@ -519,106 +540,148 @@ __global__ void __launch_bounds__(kPThreads)
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {
-    // ---------------------------------------------------- TMA producer --
+    // ----------------------------------------------------- weight copies --
     if (elect_one()) {
-      auto load_a = [&](int i) {  // K step i of this slice
-        const int s = i % sp.stages, k = (kb0 + i) * kFK;
-        const uint32_t st = smem_u32(tiles + s * sp.stage_bytes), fb = smem_u32(&full[s]);
-        mbar_arrive_expect_tx(fb, static_cast<uint32_t>((sp.tile_rows + prm.n) * kFK * 2));
-        if (EPI == kGateUp) {
-          tma_load_4d(st, &tmA, fb, k, 0, 0, row / 32);
-        } else if (A_MN) {
-          for (int m = 0; m < sp.tile_rows; m += 64) tma_load_2d(st + m / 64 * kFSlab, &tmA, fb, row + m, k);
-        } else {
-          tma_load_2d(st, &tmA, fb, k, row);
+      if (!sp.early) griddep_wait();
+      const uint32_t bytes = static_cast<uint32_t>((sp.tile_rows + prm.n) * kPK * 2);  // with the tokens'
+      const uint32_t sub = static_cast<uint32_t>(sp.tile_rows * kFK * 2);  // a K step's rows
+      int s = 0, i = 0;
+      uint32_t phase = 1;
+      for (; i < steps; ++i) {
+        if (i >= sp.stages && !mbar_wait(empty0 + s * 8, phase, abort_flag, prm.err)) break;
+        const uint32_t st = tiles0 + static_cast<uint32_t>(s * sp.stage_bytes), fb = full0 + s * 8;
+        mbar_arrive_expect_tx(fb, bytes);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = k0 + i * kPK + h * kFK;
+          if (EPI == kGateUp) {
+            tma_load_4d(st + h * sub, &tmA, fb, k, 0, 0, row / 32);
+          } else if (A_MN) {
+            tma_load_2d(st + h * sub, &tmA, fb, row, k);
+            if (sp.tile_rows > 64) tma_load_2d(st + h * sub + kFSlab, &tmA, fb, row + 64, k);
+          } else {
+            tma_load_2d(st + h * sub, &tmA, fb, k, row);
+          }
         }
-      };
-      const int steps = kb1 - kb0;
-      const int early = sp.early ? min(sp.stages, steps) : 0;
-      for (int i = 0; i < early; ++i) load_a(i);
-      griddep_wait();
-      int issued = early;  // steps whose stage is armed
-      for (int i = 0; i < steps; ++i) {
-        const int s = i % sp.stages;
-        if (i >= early) {
-          if (!mbar_wait(smem_u32(&empty[s]), (i / sp.stages & 1) ^ 1, abort_flag, prm.err)) break;
-          load_a(i);
-          issued = i + 1;
+        if (++s == sp.stages) {
+          s = 0;
+          phase ^= 1u;
         }
-        tma_load_2d(smem_u32(tiles + s * sp.stage_bytes + sp.b_off), &tmB, smem_u32(&full[s]), (kb0 + i) * kFK, col);
       }
       if (*abort_flag) {  // every copy this CTA started lands before it exits
-        for (int i = max(0, issued - sp.stages); i < issued; ++i)
-          mbar_wait(smem_u32(&full[i % sp.stages]), i / sp.stages & 1, nullptr, prm.err);
+        for (int j = max(0, i - sp.stages); j < i; ++j)
+          mbar_wait(full0 + j % sp.stages * 8, j / sp.stages & 1, nullptr, prm.err);
       }
+      if (sp.early) griddep_wait();
+    } else {
+      return;  // see the pair kernel: a thread alone in its warp
     }
-    __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------ MMA issuer --
+    // ------------------------------------------------------- MMA issuer --
     if (elect_one()) {
-      const uint32_t idesc = idesc_bf16_f32(kFM, prm.n) | (A_MN ? kIdescAMn : 0u);
-      for (int i = 0; i < kb1 - kb0; ++i) {
-        const int s = i % sp.stages;
-        if (!mbar_wait(smem_u32(&full[s]), i / sp.stages & 1, abort_flag, prm.err)) break;
+      const uint32_t idesc = idesc_bf16_f32(sp.mma_rows, prm.n) | (A_MN ? kIdescAMn : 0u);
+      // Descriptors advance by additions to their address field (16-byte units).
+      const uint64_t a_first = A_MN ? sdesc_sw128_mn(tiles0, kFSlab) : sdesc_sw128(tiles0);
+      const uint64_t b_first = sdesc_sw128(tiles0 + sp.b_off);
+      const uint32_t a_sub = static_cast<uint32_t>(sp.tile_rows * kFK * 2) / 16;
+      const uint32_t b_sub = static_cast<uint32_t>(prm.n * kFK * 2) / 16;
+      uint32_t at = 0, stage = 0, phase = 0;
+      for (int i = 0; i < steps; ++i) {
+        if (!mbar_wait(full0 + stage * 8, phase, abort_flag, prm.err)) break;
         tc_fence_after();
-        const uint32_t a0 = smem_u32(tiles + s * sp.stage_bytes), b0 = a0 + sp.b_off;
 #pragma unroll
-        for (int k = 0; k < kFK / 16; ++k)
-          umma_f16(tmem_base, A_MN ? sdesc_sw128_mn(a0 + k * 2048, kFSlab) : sdesc_sw128(a0 + k * 32),
-                   sdesc_sw128(b0 + k * 32), idesc, (i | k) ? 1u : 0u);
-        umma_commit(smem_u32(&empty[s]));
+        for (int k = 0; k < kPK / 16; ++k)
+          umma_f16(tmem_base, a_first + (at + k / 4 * a_sub + k % 4 * (A_MN ? 2048 : 32) / 16),
+                   b_first + (at + k / 4 * b_sub + k % 4 * 2), idesc, (i | k) ? 1u : 0u);
+        umma_commit(empty0 + stage * 8);
+        at += static_cast<uint32_t>(sp.stage_bytes) / 16;
+        if (++stage == static_cast<uint32_t>(sp.stages)) {
+          stage = 0;
+          phase ^= 1u;
+          at = 0;
+        }
       }
       umma_commit(smem_u32(done));
+      // Only this thread polls for the accumulator; the rest of the CTA sleeps
+      // at the block barrier below.  After an abort the MMAs that were issued
+      // still complete.
+      if (!mbar_wait(smem_u32(done), 0, nullptr, prm.err)) *abort_flag = 1;
+      tc_fence_before();
+      griddep_wait();
+    } else {
+      return;
     }
-    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------ token copies --
+    if (elect_one()) {
+      griddep_wait();
+      int s = 0;
+      uint32_t phase = 1;
+      for (int i = 0; i < steps; ++i) {
+        if (i >= sp.stages && !mbar_wait(empty0 + s * 8, phase, abort_flag, prm.err)) break;
+        const uint32_t st = tiles0 + static_cast<uint32_t>(s * sp.stage_bytes + sp.b_off);
+        tma_load_2d(st, &tmB, full0 + s * 8, k0 + i * kPK, col);
+        tma_load_2d(st + static_cast<uint32_t>(prm.n * kFK * 2), &tmB, full0 + s * 8, k0 + i * kPK + kFK, col);
+        if (++s == sp.stages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+    } else {
+      return;
+    }
+  } else {
+    griddep_wait();
   }
-  griddep_wait();
   // the dependent kernel may start: everything before this one has finished
   griddep_launch_dependents();
   // ---------------------------------------------------------- epilogue --
-  // (also after an abort: the MMAs that were issued complete)
-  const bool ok = __syncthreads_and(mbar_wait(smem_u32(done), 0, nullptr, prm.err) && !*abort_flag) != 0;
+  __syncthreads();
+  const bool ok = *abort_flag == 0;
   tc_fence_after();
-  if (warp >= 2 && ok) {
-    const int q = warp & 3;
-    if (q * 32 < sp.tile_rows) {
+  const int feats = sp.tile_rows / kHalves, ncols = min(prm.n, prm.cols - col);
+  if (warp >= 3 && ok) {
+    // this warp's accumulator rows: 32, or 16 of an M=64 MMA (on lanes 0-15)
+    const int q = warp & 3, per_warp = sp.mma_rows / 4;
+    if (q * per_warp < sp.tile_rows) {
       const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-      for (int c = 0; c < prm.n; c += 16) {
+      float *to = part + q * per_warp + lane;
+      for (int c = 0; c < ncols; c += 16) {
         uint32_t d[16];
         tmem_ld16(t + c, d);
         tmem_ld_wait();
+        if (lane < per_warp) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * sp.tile_rows + q * 32 + lane] = __uint_as_float(d[j]);
+          for (int j = 0; j < 16; ++j) to[(c + j) * sp.tile_rows] = __uint_as_float(d[j]);
+        }
       }
     }
   }
   tc_fence_before();
-  if (slices > 1) cluster_sync_all();
+  if (slices > 1) cluster_sync_rest();
   else __syncthreads();
-  if (warp == 1) {
+  if (warp == 3) {
     tc_fence_after();
     tmem_dealloc(tmem_base, tmem_cols);
   }
-  if (ok) {
-    // this CTA's share of the tile's elements, features fastest
-    const int feats = EPI == kGateUp ? sp.tile_rows / 2 : sp.tile_rows;
-    const int f0 = EPI == kGateUp ? row / 2 : row;
-    const int items = feats * min(prm.n, prm.cols - col);
-    const int per = (items + slices * 32 - 1) / (slices * 32) * 32;
-    const int end = min(items, (rank + 1) * per);
-    uint32_t base[kPMaxSlices];
-#pragma unroll
-    for (int s = 0; s < kPMaxSlices; ++s) base[s] = s < slices ? mapa_shared(smem_u32(part), s) : 0u;
-    for (int i = rank * per + static_cast<int>(threadIdx.x); i < end; i += kPThreads) {
-      const int f = i % feats, c = i / feats;
-      const int r = EPI == kGateUp ? f / 16 * 32 + f % 16 : f;
-      const uint32_t at = static_cast<uint32_t>((c * sp.tile_rows + r) * 4);
+  // this thread's elements (none for the TMA and MMA threads)
+  const int f0 = row / kHalves, end = min((rank + 1) * sp.share, feats * ncols);
+  const int first = warp >= 3 && ok ? rank * sp.share + static_cast<int>(threadIdx.x) - 96 : end;
+  // an element's place in the partial tile (gate/up: its gate row's; the up row is 16 further)
+  auto place = [&](int e) {
+    const int f = e % feats;
+    return e / feats * sp.tile_rows + (EPI == kGateUp ? f / 16 * 32 + f % 16 : f);
+  };
+  if (slices > 1) {
+    // this CTA's share: sums into its own partial tile, in whose share no other CTA reads
+    for (int e = first; e < end; e += 128) {
+      const uint32_t at = smem_u32(part + place(e));
       float v[kPMaxSlices], w[kPMaxSlices];
 #pragma unroll
       for (int s = 0; s < kPMaxSlices; ++s)
         if (s < slices) {
-          v[s] = ld_cluster_f32(base[s] + at);
-          if (EPI == kGateUp) w[s] = ld_cluster_f32(base[s] + at + 64);
+          v[s] = ld_cluster_f32(mapa_shared(at, s));
+          if (EPI == kGateUp) w[s] = ld_cluster_f32(mapa_shared(at + 64, s));
         }
       float d = 0.0f, up = 0.0f;
 #pragma unroll
@@ -627,10 +690,18 @@ __global__ void __launch_bounds__(kPThreads)
           d = __fadd_rn(d, v[s]);
           if (EPI == kGateUp) up = __fadd_rn(up, w[s]);
         }
-      if (f0 + f < prm.rows) ffn_store_one<EPI>(prm, f0 + f, col + c, d, up);
+      part[place(e)] = d;
+      if (EPI == kGateUp) part[place(e) + 16] = up;
     }
+    cluster_arrive();  // done with the others' tiles; the stores below overlap the barrier
   }
-  if (slices > 1) cluster_sync_all();  // no CTA leaves while another reads its partials
+  for (int e = first; e < end; e += 128) {
+    const int f = f0 + e % feats;
+    const float *v = part + place(e);
+    if (f < prm.rows)
+      ffn_store_one<EPI>(prm, f, col + e / feats, __fadd_rn(0.0f, v[0]), EPI == kGateUp ? __fadd_rn(0.0f, v[16]) : 0.0f);
+  }
+  if (slices > 1) cluster_wait();  // no CTA leaves while another reads its partials
 }
 
 // ------------------------------------------------------------------- host --
@@ -719,7 +790,7 @@ int set_ffn_schedule(int mode) { return g_ffn_schedule.exchange(mode); }
 
 static bool use_split(int64_t M, int64_t K) {
   const int mode = g_ffn_schedule.load();
-  return mode != 1 && (K + kSliceK - 1) / kSliceK <= kPMaxSlices && (mode == 2 || M <= 256);
+  return mode != 1 && (K + kSliceK - 1) / kSliceK <= kPMaxSlices && (mode == 2 || M <= kPMaxN);
 }
 
 // The split kernel over `rows` rows of A (gate/up: 2I interleaved ones) and M
@@ -731,7 +802,7 @@ static bi_status launch_split(FfnGemm g, int64_t rows, int64_t M, int64_t K, boo
   g.nkb = div_up(K, kFK);
   g.slice_kb = kSliceK / kFK;
   g.cols = static_cast<int>(M);
-  g.n = static_cast<int>(std::min<int64_t>(256, (M + 15) / 16 * 16));
+  g.n = static_cast<int>(std::min<int64_t>(kPMaxN, (M + 15) / 16 * 16));
   g.err = device_error_word();
   p.g = g;
   const int slices = div_up(K, kSliceK), token_tiles = div_up(M, g.n);
@@ -740,14 +811,15 @@ static bi_status launch_split(FfnGemm g, int64_t rows, int64_t M, int64_t K, boo
   while (p.tile_rows > (A_MN ? 64 : 32) &&
          static_cast<int64_t>(div_up(rows, p.tile_rows)) * slices * token_tiles * 5 < num_sms() * 4)
     p.tile_rows /= 2;
-  p.b_off = p.tile_rows * kFK * 2;
-  p.stage_bytes = p.b_off + g.n * kFK * 2;
+  p.mma_rows = p.tile_rows > 64 ? 128 : 64;
+  p.b_off = p.tile_rows * kPK * 2;
+  p.stage_bytes = p.b_off + g.n * kPK * 2;
+  p.share = div_up(p.tile_rows / (EPI == kGateUp ? 2 : 1) * g.n, slices * 32) * 32;
   p.early = early;
-  // the MMA reads 128 rows (16 KB) from every stage's start
-  const int limit = g.n <= 64 ? 112 * 1024 : 227 * 1024;
-  p.stages = std::min({kPMaxStages, std::min(g.nkb, g.slice_kb), (limit - 2048 - kFABytes) / p.stage_bytes});
-  const int partial = g.n * p.tile_rows * 4;
-  const int smem = 2048 + std::max(p.stages * p.stage_bytes + kFABytes, partial);
+  // the MMA reads mma_rows rows from every K step's start, for a lower tile past its end
+  const int pad = (p.mma_rows - p.tile_rows) * kFK * 2;
+  p.stages = std::min({kPMaxStages, div_up(g.nkb, 2), (kPSmem - 2048 - pad) / p.stage_bytes});
+  const int smem = 2048 + std::max(p.stages * p.stage_bytes + pad, g.n * p.tile_rows * 4);
   if (token_tiles > 65535) {
     set_error("feed-forward product with %d token tiles", token_tiles);
     return BI_ERR_UNSUPPORTED;
@@ -760,7 +832,7 @@ static bi_status launch_split(FfnGemm g, int64_t rows, int64_t M, int64_t K, boo
   {
     std::lock_guard<std::mutex> lk(mu);
     if (setup.pending(dev)) {
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem);
       if (e != cudaSuccess) {
         cudaGetLastError();
         set_error("cudaFuncSetAttribute: %s", cudaGetErrorString(e));

@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
-  if (warp == 1) {
+  if (warp == 2) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -259,6 +259,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
   // scale tiles of the tokens col .. col + n - 1 that exist
   auto row_tiles = [&](int col) { return min(prm.x_row_tiles, (col + prm.n + 127) / 128) - col / 128; };
 
+  // the TMA and the MMA thread are alone in their warps: branches and barrier
+  // waits of a lane that others wait for are several times slower
   if (warp == 0) {
     // ---------------------------------------------------- TMA producer --
     if (elect_one()) {
@@ -297,8 +299,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
         for (int s = 0; s < prm.stages; ++s)
           if ((issued_mask >> s) & 1u) mbar_wait(smem_u32(&full[s]), (issued_parity >> s) & 1u, nullptr, prm.err);
       }
+    } else {
+      return;
     }
-    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------ MMA issuer --
     if (elect_one()) {
@@ -351,8 +354,9 @@ __global__ void __launch_bounds__(kXThreads, 1)
         umma_commit(smem_u32(drain));
         mbar_wait(smem_u32(drain), 0, nullptr, prm.err);
       }
+    } else {
+      return;
     }
-    __syncwarp();
   } else {
     // -------------------------------------------------------- epilogue --
     const int q = warp & 3, h = (warp - 2) >> 2;
@@ -360,7 +364,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
     int buf = 0;
     uint32_t buf_phase = 0;
     for (int tile = unit0; tile < total; tile += nunits) {
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&tfull[buf]), buf_phase, abort_flag, prm.err) ? 1 : 0)) break;
+      // one lane polls: 256 polling threads slow the MMA thread's own waits
+      int landed = 1;
+      if (lane == 0) landed = mbar_wait(smem_u32(&tfull[buf]), buf_phase, abort_flag, prm.err) ? 1 : 0;
+      if (!__shfl_sync(0xffffffffu, landed, 0)) break;
       tc_fence_after();
       const int row = row_of(tile), col0 = col_of(tile) + h * ncols;
       // a tile of 32 or 64 rows sits at its place among the 128
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
   }
