@@ -459,6 +459,7 @@ constexpr int kPK = 2 * kFK;        // reduction step of a stage
 constexpr int kPMaxStages = kSliceK / kPK;
 constexpr int kPMaxN = 64;          // tokens per tile
 constexpr int kPSmem = 112 * 1024;
+constexpr int kPBatch = 4;          // elements that an epilogue thread handles at once
 
 struct FfnSplit {
   FfnGemm g;
@@ -469,10 +470,27 @@ struct FfnSplit {
   int early;              // A may be read before the predecessor has finished
 };
 
-// One finished element of the result: D[row, col] (gate/up: the gate value and
-// `up` of feature `row`).
+// What an element's epilogue reads besides its sums, loaded apart from its use.
+struct Extra {
+  float a, b;
+};
+
 template <FfnEpi EPI>
-__device__ __forceinline__ void ffn_store_one(const FfnGemm &p, int f, int t, float d, float up) {
+__device__ __forceinline__ Extra ffn_extra(const FfnGemm &p, int f, int t) {
+  Extra x = {0.0f, 0.0f};
+  if constexpr (EPI == kStore) {
+    if (p.addend) x.a = __bfloat162float(p.addend[t * p.ld_add + f]);
+  } else if constexpr (EPI == kDact) {
+    const float *gu = p.gu + static_cast<int64_t>(t) * 2 * p.rows + f;
+    x.a = gu[0];
+    x.b = gu[p.rows];
+  }
+  return x;
+}
+
+// One finished element of the result: D[f, t] (gate/up: the gate value and `up`).
+template <FfnEpi EPI>
+__device__ __forceinline__ void ffn_store_one(const FfnGemm &p, int f, int t, float d, float up, Extra x) {
   if constexpr (EPI == kGateUp) {
     static_cast<__nv_bfloat16 *>(p.out)[t * p.ldo + f] = __float2bfloat16_rn(silu_mul(d, up));
     if (p.gu) {
@@ -481,14 +499,12 @@ __device__ __forceinline__ void ffn_store_one(const FfnGemm &p, int f, int t, fl
       gu[p.rows] = up;
     }
   } else if constexpr (EPI == kStore) {
-    if (p.addend) d = __fadd_rn(d, __bfloat162float(p.addend[t * p.ld_add + f]));
+    if (p.addend) d = __fadd_rn(d, x.a);
     static_cast<__nv_bfloat16 *>(p.out)[t * p.ldo + f] = __float2bfloat16_rn(d);
   } else {
-    const int64_t at = static_cast<int64_t>(t) * 2 * p.rows + f;
-    const float g = p.gu[at], u = p.gu[at + p.rows];
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + at;
-    o[0] = __float2bfloat16_rn(dgate(d, g, u));
-    o[p.rows] = __float2bfloat16_rn(dup(d, g));
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + static_cast<int64_t>(t) * 2 * p.rows + f;
+    o[0] = __float2bfloat16_rn(dgate(d, x.a, x.b));
+    o[p.rows] = __float2bfloat16_rn(dup(d, x.a));
   }
 }
 
@@ -538,6 +554,22 @@ __global__ void __launch_bounds__(kPThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+
+  // Elements of the tile, features fastest; this CTA finishes `share` of them,
+  // this thread every 128th from `first` (the TMA and MMA threads none), in
+  // batches whose loads are in flight together.
+  const int feats_log = 31 - __clz(sp.tile_rows / kHalves), feats = 1 << feats_log;
+  const int f0 = row / kHalves, ncols = min(prm.n, prm.cols - col);
+  const int end = min((rank + 1) * sp.share, feats * ncols);
+  const int first = warp >= 3 ? rank * sp.share + static_cast<int>(threadIdx.x) - 96 : end;
+  auto valid = [&](int e) { return e < end && f0 + (e & (feats - 1)) < prm.rows; };
+  auto extra_of = [&](int e) { return ffn_extra<EPI>(prm, f0 + (e & (feats - 1)), col + (e >> feats_log)); };
+  // an element's place in the partial tile (gate/up: its gate row's; the up row is 16 further)
+  auto place = [&](int e) {
+    const int f = e & (feats - 1);
+    return (e >> feats_log) * sp.tile_rows + (EPI == kGateUp ? f / 16 * 32 + f % 16 : f);
+  };
+  Extra extra[kPBatch];  // of the first batch
 
   if (warp == 0) {
     // ----------------------------------------------------- weight copies --
@@ -632,6 +664,9 @@ __global__ void __launch_bounds__(kPThreads)
     }
   } else {
     griddep_wait();
+#pragma unroll
+    for (int u = 0; u < kPBatch; ++u)
+      if (valid(first + u * 128)) extra[u] = extra_of(first + u * 128);
   }
   // the dependent kernel may start: everything before this one has finished
   griddep_launch_dependents();
@@ -639,7 +674,6 @@ __global__ void __launch_bounds__(kPThreads)
   __syncthreads();
   const bool ok = *abort_flag == 0;
   tc_fence_after();
-  const int feats = sp.tile_rows / kHalves, ncols = min(prm.n, prm.cols - col);
   if (warp >= 3 && ok) {
     // this warp's accumulator rows: 32, or 16 of an M=64 MMA (on lanes 0-15)
     const int q = warp & 3, per_warp = sp.mma_rows / 4;
@@ -664,42 +698,53 @@ __global__ void __launch_bounds__(kPThreads)
     tc_fence_after();
     tmem_dealloc(tmem_base, tmem_cols);
   }
-  // this thread's elements (none for the TMA and MMA threads)
-  const int f0 = row / kHalves, end = min((rank + 1) * sp.share, feats * ncols);
-  const int first = warp >= 3 && ok ? rank * sp.share + static_cast<int>(threadIdx.x) - 96 : end;
-  // an element's place in the partial tile (gate/up: its gate row's; the up row is 16 further)
-  auto place = [&](int e) {
-    const int f = e % feats;
-    return e / feats * sp.tile_rows + (EPI == kGateUp ? f / 16 * 32 + f % 16 : f);
-  };
   if (slices > 1) {
     // this CTA's share: sums into its own partial tile, in whose share no other CTA reads
-    for (int e = first; e < end; e += 128) {
-      const uint32_t at = smem_u32(part + place(e));
-      float v[kPMaxSlices], w[kPMaxSlices];
+    for (int e0 = first; ok && e0 < end; e0 += kPBatch * 128) {
+      float v[kPBatch][kPMaxSlices], w[kPBatch][kPMaxSlices];
 #pragma unroll
-      for (int s = 0; s < kPMaxSlices; ++s)
-        if (s < slices) {
-          v[s] = ld_cluster_f32(mapa_shared(at, s));
-          if (EPI == kGateUp) w[s] = ld_cluster_f32(mapa_shared(at + 64, s));
-        }
-      float d = 0.0f, up = 0.0f;
+      for (int s = 0; s < kPMaxSlices; ++s) {
+        if (s >= slices) break;
+        const uint32_t tile = mapa_shared(smem_u32(part), s);
 #pragma unroll
-      for (int s = 0; s < kPMaxSlices; ++s)
-        if (s < slices) {
-          d = __fadd_rn(d, v[s]);
-          if (EPI == kGateUp) up = __fadd_rn(up, w[s]);
+        for (int u = 0; u < kPBatch; ++u) {
+          if (e0 + u * 128 >= end) break;
+          const uint32_t at = tile + static_cast<uint32_t>(place(e0 + u * 128)) * 4;
+          v[u][s] = ld_cluster_f32(at);
+          if (EPI == kGateUp) w[u][s] = ld_cluster_f32(at + 64);
         }
-      part[place(e)] = d;
-      if (EPI == kGateUp) part[place(e) + 16] = up;
+      }
+#pragma unroll
+      for (int u = 0; u < kPBatch; ++u) {
+        if (e0 + u * 128 >= end) break;
+        float d = 0.0f, up = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kPMaxSlices; ++s) {
+          if (s >= slices) break;
+          d = __fadd_rn(d, v[u][s]);
+          if (EPI == kGateUp) up = __fadd_rn(up, w[u][s]);
+        }
+        float *to = part + place(e0 + u * 128);
+        to[0] = d;
+        if (EPI == kGateUp) to[16] = up;
+      }
     }
     cluster_arrive();  // done with the others' tiles; the stores below overlap the barrier
   }
-  for (int e = first; e < end; e += 128) {
-    const int f = f0 + e % feats;
-    const float *v = part + place(e);
-    if (f < prm.rows)
-      ffn_store_one<EPI>(prm, f, col + e / feats, __fadd_rn(0.0f, v[0]), EPI == kGateUp ? __fadd_rn(0.0f, v[16]) : 0.0f);
+  for (int e0 = first; ok && e0 < end; e0 += kPBatch * 128) {
+    if (e0 != first) {
+#pragma unroll
+      for (int u = 0; u < kPBatch; ++u)
+        if (valid(e0 + u * 128)) extra[u] = extra_of(e0 + u * 128);
+    }
+#pragma unroll
+    for (int u = 0; u < kPBatch; ++u) {
+      const int e = e0 + u * 128;
+      const float *v = part + place(e);
+      if (valid(e))
+        ffn_store_one<EPI>(prm, f0 + (e & (feats - 1)), col + (e >> feats_log), __fadd_rn(0.0f, v[0]),
+                           EPI == kGateUp ? __fadd_rn(0.0f, v[16]) : 0.0f, extra[u]);
+    }
   }
   if (slices > 1) cluster_wait();  // no CTA leaves while another reads its partials
 }
