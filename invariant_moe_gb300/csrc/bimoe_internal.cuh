@@ -60,6 +60,9 @@ bool make_tma_2d_bf16_ld(CUtensorMap *map, const void *base, uint64_t rows, uint
                          uint32_t box_rows);
 // Encode a 2-D byte map over a row-major [rows, row_bytes] array with a
 // [box_rows, 128]-byte box, 128-byte swizzle.
+// Encode a 2-D map over mx4 scale tiles [row_tiles][ktiles * 512 bytes] with a
+// box of two k tiles (1024 bytes) of box_rows row tiles, not swizzled.
+bool make_tma_mx_scales(CUtensorMap *map, const void *base, uint64_t row_tiles, uint64_t ktiles, uint32_t box_rows);
 bool make_tma_2d_u8(CUtensorMap *map, const void *base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows);
 bool make_tma_2d_f32(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                      uint32_t box_rows);
@@ -437,14 +440,6 @@ __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// Untiled copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
-// to this CTA's shared memory.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
 // ---- tcgen05 (5th-generation tensor cores, tensor memory)
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
@@ -487,6 +482,22 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint
           d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
       : "memory");
+}
+// The same over a CTA pair (cta_group::2): each CTA's tensor memory holds the
+// scales of its own rows of A and of all columns of B.
+__device__ __forceinline__ void umma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+// In both CTAs of a pair, each from its own shared memory.
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t taddr, uint64_t s_desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
 }
 // Copy a 512-byte scale tile (32 lanes x 16 bytes) from shared memory to four
 // tensor-memory columns, repeated in the four lane quarters.  Ordered before

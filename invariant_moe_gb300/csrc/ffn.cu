@@ -66,10 +66,6 @@ struct FfnGemm {
   int *err;
 };
 
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  return __fmul_rn(__fdividef(g, __fadd_rn(1.0f, __expf(-g))), u);
-}
-
 // The two projections' gradients from dact = d: one fixed fp32 sequence.
 __device__ __forceinline__ float gate_sigmoid(float g) { return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-g))); }
 __device__ __forceinline__ float dgate(float d, float g, float u) {

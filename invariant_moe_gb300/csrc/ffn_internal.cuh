@@ -7,6 +7,13 @@
 
 namespace bimoe {
 
+// silu(g) * u: one fixed fp32 sequence (the fast exponential and divide are
+// within a few ulp of fp32, far below the bf16 rounding that follows; for g
+// below about -87 the denominator overflows and the quotient is the limit, 0).
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return __fmul_rn(__fdividef(g, __fadd_rn(1.0f, __expf(-g))), u);
+}
+
 // A row-major bf16 matrix [rows, cols] with row stride ld (elements).
 struct Mat {
   const __nv_bfloat16 *p;

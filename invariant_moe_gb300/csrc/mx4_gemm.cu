@@ -1,0 +1,496 @@
+// mx4_gemm.cu -- product of two matrices in the microscaled 4-bit form, plain
+// or gated, on the block-scaled tensor-core path.
+//
+//   y = X W^T (+ addend),  or  act = silu(X Wg^T) * (X Wu^T)
+//
+// tcgen05.mma kind::mxf4 takes both operands as 4-bit codes and applies the
+// scales itself, 64 k per MMA, summing in fp32.
+//   * Weight rows are the MMA's rows, tokens its columns.  A stage is 256 k:
+//     128-byte rows of codes by TMA (128-byte swizzle) and the scale tiles by
+//     TMA, which tcgen05.cp spreads into tensor memory before the MMAs that use
+//     them (cp and MMAs of one thread execute in order).
+//   * One chain of MMAs over increasing k per output, whatever the tile: a
+//     token's row has the same bits in every batch.
+//   * Many tokens: CTA pairs (cta_group::2), 256 weight rows x up to 256 tokens,
+//     each CTA staging its own rows of W and half of the tokens.  Few: one CTA
+//     with 128, 64 or 32 weight rows (at their places in the 128-row scale tile)
+//     x up to 128 tokens, so that more CTAs stream the weights.
+//   * Two accumulators of 256 columns and the scales do not fit the 512 columns
+//     of tensor memory: the second starts at column 224, and the epilogue drains
+//     the 32 shared columns first and then lets the next tile's MMAs go.
+//   * Eight epilogue warps, 32 rows x half of the columns each, take the tile to
+//     registers before anything is stored.
+#include <mutex>
+
+#include "ffn_internal.cuh"
+
+namespace bimoe {
+
+constexpr int kXThreads = 384;       // TMA and MMA warps (two idle), 8 epilogue warps
+constexpr int kXRegsFew = 40, kXRegsMany = 232;  // 168 at launch: 128 x 40 + 256 x 232 = 384 x 168
+constexpr int kXRows = 128;          // weight rows per CTA
+constexpr int kXStageK = 256;        // values of k per stage
+constexpr int kXABytes = kXRows * kXStageK / 2;
+constexpr int kXMaxStages = 12;
+constexpr int kXAcc = 224;           // tensor-memory column of the second accumulator
+constexpr int kXSfA = 480;           // scales of A: 4 columns per 128 k
+constexpr int kXSfB = 488;           // scales of B: 8 columns (two row tiles) per 128 k
+constexpr int kXSmem = 227 * 1024;
+
+struct Mx4Gemm {
+  int M, N;             // tokens, weight rows
+  int nkb;              // stages of the reduction
+  int n64;              // MMAs of the reduction
+  int rows;             // weight rows per tile (pair: 256)
+  int n;                // tokens per tile (the MMA's N)
+  int sfb_tiles;        // scale tiles (128 tokens) that a token tile touches
+  int m_tiles, n_tiles;
+  int stages, stage_bytes;
+  __nv_bfloat16 *y;
+  int64_t ldy;
+  const __nv_bfloat16 *addend;
+  int64_t ld_add;
+  int *err;
+};
+
+// Epilogue of one warp: acc[c] = D[row0 + lane, col0 + c], c < ncols.
+template <bool GATED, int COLS>
+__device__ __forceinline__ void mx4_epilogue(const Mx4Gemm &p, const float (&acc)[COLS], int row0, int col0, int ncols,
+                                             int lane) {
+  const int limit = min(ncols, p.M - col0);
+  if (limit <= 0) return;
+  if (GATED) {
+    // lanes 0-15 hold the gate values of 16 features, lanes 16-31 their up values
+    const int f = row0 / 2 + (lane & 15);
+    const bool is_gate = lane < 16, ok = 2 * f < p.N;
+    __nv_bfloat16 *y = p.y + static_cast<int64_t>(col0) * p.ldy + f;
+#pragma unroll
+    for (int c = 0; c < COLS; c += 16) {
+      if (c >= limit) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // the gate lane finishes columns c..c+7, the up lane c+8..c+15
+        const float keep = is_gate ? acc[c + j] : acc[c + 8 + j];
+        const float other = __shfl_xor_sync(0xffffffffu, is_gate ? acc[c + 8 + j] : acc[c + j], 16);
+        const int n = c + (is_gate ? j : 8 + j);
+        const float g = is_gate ? keep : other, u = is_gate ? other : keep;
+        if (ok && n < limit) y[n * p.ldy] = __float2bfloat16_rn(silu_mul(g, u));
+      }
+    }
+    return;
+  }
+  const int f = row0 + lane;
+  if (f >= p.N) return;
+  __nv_bfloat16 *y = p.y + static_cast<int64_t>(col0) * p.ldy + f;
+  if (p.addend) {
+    // the next 16 columns' addends are loaded while these are stored
+    const __nv_bfloat16 *a = p.addend + static_cast<int64_t>(col0) * p.ld_add + f;
+    __nv_bfloat16 add[2][16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) add[0][j] = a[min(j, limit - 1) * p.ld_add];
+#pragma unroll
+    for (int c = 0; c < COLS; c += 16) {
+      if (c >= limit) break;
+      if (c + 16 < limit) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) add[(c / 16 + 1) & 1][j] = a[min(c + 16 + j, limit - 1) * p.ld_add];
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (c + j < limit)
+          y[(c + j) * p.ldy] = __float2bfloat16_rn(__fadd_rn(acc[c + j], __bfloat162float(add[(c / 16) & 1][j])));
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < COLS; ++c)
+      if (c < limit) y[c * p.ldy] = __float2bfloat16_rn(acc[c]);
+  }
+}
+
+template <bool GATED, bool PAIR>
+__global__ void __launch_bounds__(kXThreads, 1)
+    mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                    const __grid_constant__ Mx4Gemm prm) {
+  constexpr int kCols = PAIR ? 128 : 64;  // columns of an epilogue warp
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *aux = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(aux);
+  uint64_t *empty = full + kXMaxStages;
+  uint64_t *tfull = empty + kXMaxStages;  // [2]
+  uint64_t *tempty = tfull + 2;           // the columns that both accumulators use are drained
+  uint64_t *drain = tempty + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  uint8_t *tiles = aux + 1024;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int total = prm.m_tiles * prm.n_tiles;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const int unit0 = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int nunits = PAIR ? static_cast<int>(num_clusters_x()) : static_cast<int>(gridDim.x);
+  const int b_rows = PAIR ? prm.n / 2 : prm.n;  // token rows that this CTA stages
+  const int b_off = kXABytes, sfa_off = b_off + (b_rows * 128 + 1023) / 1024 * 1024, sfb_off = sfa_off + 1024;
+  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty), tfull0 = smem_u32(tfull), tempty0 = smem_u32(tempty),
+                 tiles0 = smem_u32(tiles);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < prm.stages; ++s) {
+      mbar_init(full0 + s * 8, 1);
+      mbar_init(empty0 + s * 8, 1);
+    }
+    mbar_init(tfull0, 1);
+    mbar_init(tfull0 + 8, 1);
+    mbar_init(tempty0, PAIR ? 16 : 8);
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+  }
+  if (warp == 2) {
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), 512);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+
+  auto wait = [&](uint32_t bar, uint32_t parity, volatile int *ab) {
+    return PAIR ? mbar_wait_cl(bar, parity, ab, prm.err) : mbar_wait(bar, parity, ab, prm.err);
+  };
+  auto row_of = [&](int tile) { return tile / prm.n_tiles * prm.rows + static_cast<int>(rank) * kXRows; };
+  auto col_of = [&](int tile) { return tile % prm.n_tiles * prm.n; };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kXRegsFew));
+    // the TMA and the MMA thread are alone in their warps: branches and barrier
+    // waits of a lane that others wait for are several times slower
+    if (warp == 0) {
+      // -------------------------------------------------- TMA producer --
+      if (elect_one()) {
+        const int a_rows = PAIR ? kXRows : prm.rows;
+        const uint32_t bytes =
+            (PAIR ? 2u : 1u) * static_cast<uint32_t>((a_rows + b_rows) * 128 + (1 + prm.sfb_tiles) * 1024);
+        uint32_t stage = 0, phase = 0, issued_mask = 0, issued_parity = 0;
+        bool ok = true;
+        for (int tile = unit0; tile < total && ok; tile += nunits) {
+          const int row = row_of(tile), col = col_of(tile);
+          for (int kb = 0; kb < prm.nkb; ++kb) {
+            if (!wait(empty0 + stage * 8, phase ^ 1u, abort_flag)) {
+              ok = false;
+              break;
+            }
+            const uint32_t st = tiles0 + stage * static_cast<uint32_t>(prm.stage_bytes);
+            if (PAIR) {
+              // both CTAs' copies complete on the even CTA's barrier
+              const uint32_t fb = mapa_shared(full0 + stage * 8, 0);
+              if (rank == 0) mbar_arrive_expect_tx(full0 + stage * 8, bytes);
+              tma_load_2d_pair(st, &tmA, fb, kb * 128, row);
+              tma_load_2d_pair(st + b_off, &tmB, fb, kb * 128, col + static_cast<int>(rank) * b_rows);
+              tma_load_2d_pair(st + sfa_off, &tmSA, fb, kb * 256, row / 128);
+              tma_load_2d_pair(st + sfb_off, &tmSB, fb, kb * 256, col / 128);
+            } else {
+              const uint32_t fb = full0 + stage * 8;
+              mbar_arrive_expect_tx(fb, bytes);
+              // the rows at their places in the 128-row scale tile
+              tma_load_2d(st + static_cast<uint32_t>(row % 128) * 128, &tmA, fb, kb * 128, row);
+              tma_load_2d(st + b_off, &tmB, fb, kb * 128, col);
+              tma_load_2d(st + sfa_off, &tmSA, fb, kb * 256, row / 128);
+              tma_load_2d(st + sfb_off, &tmSB, fb, kb * 256, col / 128);
+            }
+            issued_mask |= 1u << stage;
+            issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+            if (++stage == static_cast<uint32_t>(prm.stages)) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        if (*abort_flag) {  // every copy this CTA started lands before it exits
+          if (rank == 0) {
+            for (int s = 0; s < prm.stages; ++s)
+              if ((issued_mask >> s) & 1u) wait(full0 + s * 8, (issued_parity >> s) & 1u, nullptr);
+          }
+          if (PAIR) {
+            // the odd CTA's copies complete on the even CTA's barriers: give them time to land
+            const unsigned long long t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 200000ull) {
+            }
+          }
+        }
+      } else {
+        return;
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------- MMA issuer --
+      if (rank == 0 && elect_one()) {
+        const uint32_t m = PAIR ? 2 * kXRows : kXRows;
+        const uint32_t idesc0 = idesc_mxf4(m, prm.n, 0), idesc1 = idesc_mxf4(m, prm.n, 1);
+        const uint64_t a_first = sdesc_sw128(tiles0), b_first = sdesc_sw128(tiles0 + b_off);
+        const uint64_t sa_first = sdesc_scales(tiles0 + sfa_off), sb_first = sdesc_scales(tiles0 + sfb_off);
+        const uint32_t sfa = tmem_base + kXSfA, sfb0 = tmem_base + kXSfB;
+        uint32_t stage = 0, phase = 0, at = 0, buf = 0, buf_phase = 0, drained = 0;
+        bool ok = true, issued = false;
+        for (int tile = unit0; tile < total && ok && !*abort_flag; tile += nunits) {
+          // the last tile's columns that this accumulator shares are drained
+          // (and so, long since, is the tile that used this accumulator)
+          if (tile != unit0) {
+            if (!wait(tempty0, drained, abort_flag)) break;
+            drained ^= 1u;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + buf * kXAcc;
+          const uint32_t sfb = sfb0 + static_cast<uint32_t>(col_of(tile) % 128 / 32);  // the first tokens' column
+          for (int kb = 0; kb < prm.nkb; ++kb) {
+            if (!wait(full0 + stage * 8, phase, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const int mmas = min(4, prm.n64 - 4 * kb);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (PAIR) {
+                tmem_copy_scales_pair(sfa + 4 * c, sa_first + (at + c * 32));
+                tmem_copy_scales_pair(sfb0 + 8 * c, sb_first + (at + c * 32));
+                if (prm.sfb_tiles > 1) tmem_copy_scales_pair(sfb0 + 8 * c + 4, sb_first + (at + 64 + c * 32));
+              } else {
+                tmem_copy_scales(sfa + 4 * c, sa_first + (at + c * 32));
+                tmem_copy_scales(sfb0 + 8 * c, sb_first + (at + c * 32));
+                if (prm.sfb_tiles > 1) tmem_copy_scales(sfb0 + 8 * c + 4, sb_first + (at + 64 + c * 32));
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k >= mmas) break;
+              if (PAIR)
+                umma_mxf4_pair(d, a_first + (at + k * 2), b_first + (at + k * 2), (k & 1) ? idesc1 : idesc0,
+                               sfa + 4 * (k / 2), sfb + 8 * (k / 2), (kb | k) ? 1u : 0u);
+              else
+                umma_mxf4(d, a_first + (at + k * 2), b_first + (at + k * 2), (k & 1) ? idesc1 : idesc0,
+                          sfa + 4 * (k / 2), sfb + 8 * (k / 2), (kb | k) ? 1u : 0u);
+            }
+            if (PAIR) umma_commit_pair(empty0 + stage * 8, 0x3);
+            else umma_commit(empty0 + stage * 8);
+            issued = true;
+            at += static_cast<uint32_t>(prm.stage_bytes) / 16;
+            if (++stage == static_cast<uint32_t>(prm.stages)) {
+              stage = 0;
+              phase ^= 1u;
+              at = 0;
+            }
+          }
+          if (!ok) break;
+          if (PAIR) umma_commit_pair(tfull0 + buf * 8, 0x3);
+          else umma_commit(tfull0 + buf * 8);
+          buf ^= 1u;
+          if (buf == 0) buf_phase ^= 1u;
+        }
+        if (PAIR || (*abort_flag && issued)) {
+          // every MMA (pair: into both CTAs' tensor memory) has completed
+          if (PAIR) umma_commit_pair(smem_u32(drain), 0x3);
+          else umma_commit(smem_u32(drain));
+          wait(smem_u32(drain), 0, nullptr);
+        }
+      } else {
+        return;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kXRegsMany));
+    // -------------------------------------------------------- epilogue --
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    // columns of this warp: half of the tile's (a tile of up to 64: all for the first four warps)
+    const int ncols = prm.n > 64 ? prm.n / 2 : (h == 0 ? prm.n : 0);
+    uint32_t buf = 0, buf_phase = 0;
+    for (int tile = unit0; tile < total; tile += nunits) {
+      // one lane polls: 256 polling threads slow the MMA thread's own waits
+      int landed = 1;
+      if (lane == 0) landed = wait(tfull0 + buf * 8, buf_phase, abort_flag) ? 1 : 0;
+      if (!__shfl_sync(0xffffffffu, landed, 0)) break;
+      tc_fence_after();
+      const int row = row_of(tile), place = PAIR ? 0 : row % 128;
+      // a tile of 32 or 64 rows sits at its place among the 128
+      const bool mine = PAIR || (q * 32 >= place && q * 32 < place + prm.rows);
+      const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kXAcc +
+                         static_cast<uint32_t>(h * ncols);
+      float acc[kCols];
+      auto take = [&](int c) {
+        uint32_t d[16];
+        tmem_ld16(t + c, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[c + j] = __uint_as_float(d[j]);
+      };
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) mbar_arrive_cluster_relaxed(mapa_shared(tempty0, 0));
+          else mbar_arrive_relaxed(tempty0);
+        }
+      };
+      // first the columns that the other accumulator shares: the last 32 of the
+      // first one, the first 32 of the second
+      constexpr int kShared = 256 - kXAcc;
+      if constexpr (PAIR) {
+        if (buf == 0) {
+#pragma unroll
+          for (int c = kCols - kShared; c < kCols; c += 16)
+            if (c < ncols) take(c);
+        } else {
+#pragma unroll
+          for (int c = 0; c < kShared; c += 16)
+            if (c < ncols) take(c);
+        }
+        release();
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16)
+          if (c < ncols && (buf == 0 ? c < kCols - kShared : c >= kShared)) take(c);
+      } else {
+        // (up to 128 columns: nothing is shared, the other accumulator is free already)
+        release();
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16)
+          if (mine && c < ncols) take(c);
+      }
+      buf ^= 1u;
+      if (buf == 0) buf_phase ^= 1u;
+      if (mine && ncols > 0)
+        mx4_epilogue<GATED, kCols>(prm, acc, (PAIR ? row : row / 128 * 128) + q * 32, col_of(tile) + h * ncols, ncols,
+                                   lane);
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) {
+    // the even CTA's final commit: its last MMAs have left this CTA's memory too
+    if (rank != 0 && threadIdx.x == 96) wait(smem_u32(drain), 0, nullptr);
+    cluster_sync_rest();  // neither CTA leaves while the other may still signal its barriers
+  }
+  if (warp == 2) {
+    tc_fence_after();
+    if (PAIR) tmem_dealloc_pair(tmem_base, 512);
+    else tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// ------------------------------------------------------------------- host --
+template <bool GATED, bool PAIR>
+static bi_status launch_mx4(const CUtensorMap (&maps)[4], const Mx4Gemm &p, cudaStream_t s) {
+  static std::mutex mu;
+  static int max_units[64] = {};  // CTAs or CTA pairs resident at once, per device
+  static ContextSetup setup;      // the shared-memory attribute is per context
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) {
+    set_error("device ordinal %d out of range", dev);
+    return BI_ERR_CUDA;
+  }
+  auto kern = mx4_gemm_kernel<GATED, PAIR>;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (max_units[dev] == 0 || setup.pending(dev)) {
+      int units = num_sms();
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kXSmem);
+      if (e == cudaSuccess && PAIR) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(2 * (num_sms() / 2));
+        cfg.blockDim = dim3(kXThreads);
+        cfg.dynamicSmemBytes = kXSmem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&units, kern, &cfg);
+      }
+      if (e != cudaSuccess || units <= 0) {
+        cudaGetLastError();
+        set_error("4-bit product set-up: %s (%d units)", cudaGetErrorString(e), units);
+        return BI_ERR_CUDA;
+      }
+      max_units[dev] = units;
+      setup.done(dev);
+    }
+  }
+  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+  if (tiles > (int64_t(1) << 30)) {
+    set_error("4-bit product with %lld tiles", (long long)tiles);
+    return BI_ERR_UNSUPPORTED;
+  }
+  const int units = static_cast<int>(std::min<int64_t>(max_units[dev], tiles));
+  const size_t smem = 2048 + static_cast<size_t>(p.stages) * p.stage_bytes;
+  return launch_chained(kern, dim3(PAIR ? 2 * units : units), dim3(kXThreads), smem, s, PAIR ? 2 : 1, maps[0], maps[1],
+                        maps[2], maps[3], p);
+}
+
+static int div_up(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+bi_status launch_mx4_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws, Mat addend,
+                          __nv_bfloat16 *y, int64_t ldy, bool gated, int64_t M, int64_t N, int64_t K, cudaStream_t s) {
+  Mx4Gemm p{};
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.nkb = div_up(K, kXStageK);
+  p.n64 = div_up(K, 64);
+  p.y = y;
+  p.ldy = ldy;
+  p.addend = addend.p;
+  p.ld_add = addend.ld;
+  p.err = device_error_word();
+  // pairs when their largest tiles give at least half of them work
+  const int pairs = std::max(1, num_sms() / 2);
+  const bool pair = static_cast<int64_t>(div_up(N, 2 * kXRows)) * div_up(M, 256) * 2 >= pairs;
+  if (pair) {
+    // tokens per tile: 256, 192 or 128, the least waves x (columns + a tile's fixed cost)
+    p.rows = 2 * kXRows;
+    p.m_tiles = div_up(N, p.rows);
+    int64_t best = INT64_MAX;
+    for (int n = 256; n >= 128; n -= 64) {
+      const int64_t cost = (static_cast<int64_t>(p.m_tiles) * div_up(M, n) + pairs - 1) / pairs * (n + 32);
+      if (cost < best) {
+        best = cost;
+        p.n = n;
+      }
+    }
+    p.sfb_tiles = p.n > 128 ? 2 : 1;
+  } else {
+    // up to 128 tokens, rounded up to 16 (above 64: to 32, two halves of whole
+    // 16-column chunks), and the tallest tiles that still give every SM one
+    p.n = M > 64 ? std::min(128, div_up(M, 32) * 32) : div_up(M, 16) * 16;
+    p.sfb_tiles = 1;
+    p.rows = kXRows;
+    while (p.rows > 32 && static_cast<int64_t>(div_up(N, p.rows)) * div_up(M, p.n) < num_sms()) p.rows /= 2;
+    p.m_tiles = div_up(N, p.rows);
+  }
+  p.n_tiles = div_up(M, p.n);
+  const int b_rows = pair ? p.n / 2 : p.n;
+  p.stage_bytes = kXABytes + div_up(b_rows * 128, 1024) * 1024 + 1024 + p.sfb_tiles * 1024;
+  p.stages = std::min(kXMaxStages, (kXSmem - 2048) / p.stage_bytes);
+  CUtensorMap maps[4];
+  const int64_t ktiles = div_up(K, 128);
+  if (!make_tma_2d_u8(&maps[0], wq, N, K / 2, pair ? kXRows : p.rows) || !make_tma_2d_u8(&maps[1], xq, M, K / 2, b_rows) ||
+      !make_tma_mx_scales(&maps[2], ws, div_up(N, 128), ktiles, 1) ||
+      !make_tma_mx_scales(&maps[3], xs, div_up(M, 128), ktiles, p.sfb_tiles))
+    return BI_ERR_CUDA;
+  if (pair) return gated ? launch_mx4<true, true>(maps, p, s) : launch_mx4<false, true>(maps, p, s);
+  return gated ? launch_mx4<true, false>(maps, p, s) : launch_mx4<false, false>(maps, p, s);
+}
+
+}  // namespace bimoe

@@ -107,7 +107,9 @@ def check(got, want, bound, name):
 # tokens, features, K: one token, tile edges on every side, odd features, K
 # that ends inside a 256-, 128- and 64-value step
 GEMM = [(1, 1, 32), (1, 4096, 2048), (2, 17, 64), (5, 1001, 2080), (31, 128, 96), (33, 129, 224), (64, 255, 256),
-        (127, 384, 288), (129, 127, 512), (200, 513, 1120), (257, 300, 160), (300, 1000, 4096)]
+        (127, 384, 288), (129, 127, 512), (200, 513, 1120), (257, 300, 160), (300, 1000, 4096),
+        # enough tiles for CTA pairs, each token tile width, ragged on both sides
+        (1100, 2100, 288), (641, 3001, 1056), (2000, 1290, 640), (4100, 600, 96), (385, 4700, 32)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM)
@@ -123,7 +125,8 @@ def test_gemm(cuda, M, N, K, with_addend):
 
 
 @pytest.mark.parametrize("M,I,K", [(1, 16, 32), (1, 2048, 4096), (3, 48, 160), (33, 768, 2048), (64, 64, 256),
-                                   (130, 336, 416), (257, 128, 1024), (300, 272, 2080)])
+                                   (130, 336, 416), (257, 128, 1024), (300, 272, 2080), (1030, 1120, 544),
+                                   (700, 1520, 288)])
 def test_gate_up(cuda, M, I, K):
     import invariant_moe_gb300 as bm
     xv, xq, xs = quantized(M, K, 1.0, 11, cuda)
@@ -154,6 +157,11 @@ def test_rows_do_not_depend_on_the_batch(cuda):
     gq, gs = bm.bi_mx4_quantize(syn.normal((2 * 336, K), K ** -0.5, 33, BF).to(cuda))
     xq, xs = bm.bi_mx4_quantize(x)
     y, act = bm.bi_mx4_gemm(xq, xs, wq, ws), bm.bi_mx4_gate_up(xq, xs, gq, gs)
+    # (a matrix of 9000 more rows takes other tiles: CTA pairs)
+    big = torch.cat((x, syn.normal((9000, K), 1.0, 34, BF).to(cuda)))
+    bq, bs = bm.bi_mx4_quantize(big)
+    assert torch.equal(bm.bi_mx4_gemm(bq, bs, wq, ws)[:M], y)
+    assert torch.equal(bm.bi_mx4_gate_up(bq, bs, gq, gs)[:M], act)
     for a, n in ((0, 1), (3, 2), (9, 7), (100, 8), (1, 9), (31, 32), (64, 33), (200, 64), (77, 65), (5, 128),
                  (300, 129), (2, 257), (500, 600)):
         sq, ss = bm.bi_mx4_quantize(x[a:a + n])
