@@ -30,7 +30,7 @@
 #include <atomic>
 #include <mutex>
 
-#include "ffn_internal.cuh"
+#include "tile_epilogue.cuh"
 
 namespace bimoe {
 
@@ -44,8 +44,8 @@ constexpr int kFSlab = 64 * kFK * 2;           // an MN-major slab: 64 rows or c
 constexpr int kFAccCols = 256;
 constexpr int kFThreads = 384;                 // TMA and MMA warps (two idle), 8 epilogue warps
 // registers a thread: 168 at launch (384 x 168 = 64512); the first four warps
-// hand theirs to the epilogue's, 128 x 40 + 256 x 232 = 64512
-constexpr int kFRegsFew = 40, kFRegsMany = 232;
+// hand some of theirs to the epilogue's, 128 x 56 + 256 x 224 = 64512
+constexpr int kFRegsFew = 56, kFRegsMany = 224;
 constexpr int kFSmem = 1024 + kFStages * kFStageBytes + 256;
 constexpr int kSliceK = 1024;                  // reduction slice of the recipe
 static_assert(kFSmem <= 227 * 1024, "shared memory");
@@ -85,11 +85,6 @@ __device__ __forceinline__ void store_32b(void *p, const uint32_t (&v)[8], bool 
     q[0] = make_uint4(v[0], v[1], v[2], v[3]);
     q[1] = make_uint4(v[4], v[5], v[6], v[7]);
   }
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 // Epilogue of one warp: acc[c] = D[row, col0 + c], c < ncols (a multiple of 16), row = row0 + lane.

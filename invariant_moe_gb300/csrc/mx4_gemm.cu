@@ -22,12 +22,12 @@
 //     registers before anything is stored.
 #include <mutex>
 
-#include "ffn_internal.cuh"
+#include "tile_epilogue.cuh"
 
 namespace bimoe {
 
 constexpr int kXThreads = 384;       // TMA and MMA warps (two idle), 8 epilogue warps
-constexpr int kXRegsFew = 40, kXRegsMany = 232;  // 168 at launch: 128 x 40 + 256 x 232 = 384 x 168
+constexpr int kXRegsFew = 56, kXRegsMany = 224;  // 168 at launch: 128 x 56 + 256 x 224 = 384 x 168
 constexpr int kXRows = 128;          // weight rows per CTA
 constexpr int kXStageK = 256;        // values of k per stage
 constexpr int kXABytes = kXRows * kXStageK / 2;
@@ -53,57 +53,35 @@ struct Mx4Gemm {
   int *err;
 };
 
-// Epilogue of one warp: acc[c] = D[row0 + lane, col0 + c], c < ncols.
-template <bool GATED, int COLS>
-__device__ __forceinline__ void mx4_epilogue(const Mx4Gemm &p, const float (&acc)[COLS], int row0, int col0, int ncols,
-                                             int lane) {
+// Epilogue of one warp: 32 accumulator rows from row0, COLS/16 chunks of 16
+// tokens from col0 (v[chunk][half of the rows], tmem_ld_16x16's order).
+template <bool GATED, int CHUNKS>
+__device__ __forceinline__ void mx4_epilogue(const Mx4Gemm &p, const uint32_t (&v)[CHUNKS][2][8], int row0, int col0, int ncols,
+                                             uint32_t stage, int lane) {
   const int limit = min(ncols, p.M - col0);
-  if (limit <= 0) return;
   if (GATED) {
-    // lanes 0-15 hold the gate values of 16 features, lanes 16-31 their up values
-    const int f = row0 / 2 + (lane & 15);
-    const bool is_gate = lane < 16, ok = 2 * f < p.N;
+    // the first 16 rows are the gate values of 16 features, the others their up values
+    const int f = row0 / 2;
     __nv_bfloat16 *y = p.y + static_cast<int64_t>(col0) * p.ldy + f;
+    const RowsOut out{y, p.ldy, limit, p.N / 2 - f, rows_aligned(p.y, p.ldy)};
 #pragma unroll
-    for (int c = 0; c < COLS; c += 16) {
-      if (c >= limit) break;
+    for (int c = 0; c < CHUNKS; ++c) {
+      if (c * 16 >= limit) break;
+      float act[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // the gate lane finishes columns c..c+7, the up lane c+8..c+15
-        const float keep = is_gate ? acc[c + j] : acc[c + 8 + j];
-        const float other = __shfl_xor_sync(0xffffffffu, is_gate ? acc[c + 8 + j] : acc[c + j], 16);
-        const int n = c + (is_gate ? j : 8 + j);
-        const float g = is_gate ? keep : other, u = is_gate ? other : keep;
-        if (ok && n < limit) y[n * p.ldy] = __float2bfloat16_rn(silu_mul(g, u));
-      }
-    }
-    return;
-  }
-  const int f = row0 + lane;
-  if (f >= p.N) return;
-  __nv_bfloat16 *y = p.y + static_cast<int64_t>(col0) * p.ldy + f;
-  if (p.addend) {
-    // the next 16 columns' addends are loaded while these are stored
-    const __nv_bfloat16 *a = p.addend + static_cast<int64_t>(col0) * p.ld_add + f;
-    __nv_bfloat16 add[2][16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) add[0][j] = a[min(j, limit - 1) * p.ld_add];
-#pragma unroll
-    for (int c = 0; c < COLS; c += 16) {
-      if (c >= limit) break;
-      if (c + 16 < limit) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) add[(c / 16 + 1) & 1][j] = a[min(c + 16 + j, limit - 1) * p.ld_add];
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (c + j < limit)
-          y[(c + j) * p.ldy] = __float2bfloat16_rn(__fadd_rn(acc[c + j], __bfloat162float(add[(c / 16) & 1][j])));
+      for (int j = 0; j < 8; ++j) act[j] = silu_mul(__uint_as_float(v[c][0][j]), __uint_as_float(v[c][1][j]));
+      store_rows16(stage, act, c * 16, out, lane);
     }
   } else {
+    const RowsOut out{p.y + static_cast<int64_t>(col0) * p.ldy + row0, p.ldy, limit, p.N - row0,
+                      rows_aligned(p.y, p.ldy)};
+    const RowsOut add{const_cast<__nv_bfloat16 *>(p.addend) + static_cast<int64_t>(col0) * p.ld_add + row0, p.ld_add,
+                      limit, p.N - row0, rows_aligned(p.addend, p.ld_add)};
 #pragma unroll
-    for (int c = 0; c < COLS; ++c)
-      if (c < limit) y[c * p.ldy] = __float2bfloat16_rn(acc[c]);
+    for (int c = 0; c < CHUNKS; ++c) {
+      if (c * 16 >= limit) break;
+      store_rows32(stage, v[c], c * 16, out, p.addend ? &add : nullptr, lane);
+    }
   }
 }
 
@@ -314,25 +292,20 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const int q = warp & 3, h = (warp - 4) >> 2;
     // columns of this warp: half of the tile's (a tile of up to 64: all for the first four warps)
     const int ncols = prm.n > 64 ? prm.n / 2 : (h == 0 ? prm.n : 0);
+    const uint32_t staging = tiles0 + static_cast<uint32_t>(prm.stages * prm.stage_bytes + (warp - 4) * kStageBytes);
     uint32_t buf = 0, buf_phase = 0;
     for (int tile = unit0; tile < total; tile += nunits) {
-      // one lane polls: 256 polling threads slow the MMA thread's own waits
-      int landed = 1;
-      if (lane == 0) landed = wait(tfull0 + buf * 8, buf_phase, abort_flag) ? 1 : 0;
-      if (!__shfl_sync(0xffffffffu, landed, 0)) break;
+      if (!__all_sync(0xffffffffu, wait(tfull0 + buf * 8, buf_phase, abort_flag) ? 1 : 0)) break;
       tc_fence_after();
       const int row = row_of(tile), place = PAIR ? 0 : row % 128;
       // a tile of 32 or 64 rows sits at its place among the 128
       const bool mine = PAIR || (q * 32 >= place && q * 32 < place + prm.rows);
       const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kXAcc +
                          static_cast<uint32_t>(h * ncols);
-      float acc[kCols];
-      auto take = [&](int c) {
-        uint32_t d[16];
-        tmem_ld16(t + c, d);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) acc[c + j] = __uint_as_float(d[j]);
+      uint32_t v[kCols / 16][2][8];
+      auto take = [&](int c) {  // chunk c of 16 columns
+        tmem_ld_16x16(t + c * 16, v[c][0]);
+        tmem_ld_16x16(t + (16u << 16) + c * 16, v[c][1]);
       };
       auto release = [&] {
         tc_fence_before();
@@ -344,34 +317,35 @@ __global__ void __launch_bounds__(kXThreads, 1)
       };
       // first the columns that the other accumulator shares: the last 32 of the
       // first one, the first 32 of the second
-      constexpr int kShared = 256 - kXAcc;
+      constexpr int kChunks = kCols / 16, kShared = (256 - kXAcc) / 16;
       if constexpr (PAIR) {
         if (buf == 0) {
 #pragma unroll
-          for (int c = kCols - kShared; c < kCols; c += 16)
-            if (c < ncols) take(c);
+          for (int c = kChunks - kShared; c < kChunks; ++c)
+            if (c * 16 < ncols) take(c);
         } else {
 #pragma unroll
-          for (int c = 0; c < kShared; c += 16)
-            if (c < ncols) take(c);
+          for (int c = 0; c < kShared; ++c)
+            if (c * 16 < ncols) take(c);
         }
+        tmem_ld_wait();
         release();
 #pragma unroll
-        for (int c = 0; c < kCols; c += 16)
-          if (c < ncols && (buf == 0 ? c < kCols - kShared : c >= kShared)) take(c);
+        for (int c = 0; c < kChunks; ++c)
+          if (c * 16 < ncols && (buf == 0 ? c < kChunks - kShared : c >= kShared)) take(c);
       } else {
         // (up to 128 columns: nothing is shared, the other accumulator is free already)
         release();
 #pragma unroll
-        for (int c = 0; c < kCols; c += 16)
-          if (mine && c < ncols) take(c);
+        for (int c = 0; c < kChunks; ++c)
+          if (mine && c * 16 < ncols) take(c);
       }
+      tmem_ld_wait();
       buf ^= 1u;
       if (buf == 0) buf_phase ^= 1u;
       if (mine && ncols > 0)
-        mx4_epilogue<GATED, kCols>(prm, acc, (PAIR ? row : row / 128 * 128) + q * 32, col_of(tile) + h * ncols, ncols,
-                                   lane);
-      __syncwarp();
+        mx4_epilogue<GATED, kChunks>(prm, v, (PAIR ? row : row / 128 * 128) + q * 32, col_of(tile) + h * ncols, ncols,
+                                     staging, lane);
     }
   }
 
@@ -435,7 +409,7 @@ static bi_status launch_mx4(const CUtensorMap (&maps)[4], const Mx4Gemm &p, cuda
     return BI_ERR_UNSUPPORTED;
   }
   const int units = static_cast<int>(std::min<int64_t>(max_units[dev], tiles));
-  const size_t smem = 2048 + static_cast<size_t>(p.stages) * p.stage_bytes;
+  const size_t smem = 2048 + static_cast<size_t>(p.stages) * p.stage_bytes + 8 * kStageBytes;
   return launch_chained(kern, dim3(PAIR ? 2 * units : units), dim3(kXThreads), smem, s, PAIR ? 2 : 1, maps[0], maps[1],
                         maps[2], maps[3], p);
 }
@@ -482,7 +456,7 @@ bi_status launch_mx4_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *w
   p.n_tiles = div_up(M, p.n);
   const int b_rows = pair ? p.n / 2 : p.n;
   p.stage_bytes = kXABytes + div_up(b_rows * 128, 1024) * 1024 + 1024 + p.sfb_tiles * 1024;
-  p.stages = std::min(kXMaxStages, (kXSmem - 2048) / p.stage_bytes);
+  p.stages = std::min(kXMaxStages, (kXSmem - 2048 - 8 * kStageBytes) / p.stage_bytes);
   CUtensorMap maps[4];
   const int64_t ktiles = div_up(K, 128);
   if (!make_tma_2d_u8(&maps[0], wq, N, K / 2, pair ? kXRows : p.rows) || !make_tma_2d_u8(&maps[1], xq, M, K / 2, b_rows) ||
