@@ -46,7 +46,7 @@ constexpr int kFThreads = 384;                 // TMA and MMA warps (two idle), 
 // registers a thread: 168 at launch (384 x 168 = 64512); the first four warps
 // hand some of theirs to the epilogue's, 128 x 56 + 256 x 224 = 64512
 constexpr int kFRegsFew = 56, kFRegsMany = 224;
-constexpr int kFSmem = 1024 + kFStages * kFStageBytes + 256;
+constexpr int kFSmem = 1024 + kFStages * kFStageBytes + 256 + 8 * 16 * 144;  // ring, barriers, epilogue staging
 constexpr int kSliceK = 1024;                  // reduction slice of the recipe
 static_assert(kFSmem <= 227 * 1024, "shared memory");
 
@@ -87,116 +87,148 @@ __device__ __forceinline__ void store_32b(void *p, const uint32_t (&v)[8], bool 
   }
 }
 
-// Epilogue of one warp: acc[c] = D[row, col0 + c], c < ncols (a multiple of 16), row = row0 + lane.
+// Staging buffer of an epilogue warp: 16 tokens x 32 features, fp32 rows 144
+// bytes apart (or bf16 ones, kStagePitch).
+constexpr int kFPitch = 144;
+constexpr int kFStaging = 16 * kFPitch;
+
+// 16 tokens x 32 features of an fp32 matrix, rows 2I apart: 16-byte loads (lane:
+// token lane / 8 and every 4th further, features 4 (lane % 8) ..).
+__device__ __forceinline__ void load_rows_f32(const float *p, int64_t ld, int t0, int tokens, int feats, int lane,
+                                              float4 (&w)[4]) {
+  const float *q = p + (lane & 7) * 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + i * 4 + (lane >> 3);
+    // feats is a multiple of 16: a part is inside or outside
+    w[i] = t < tokens && (lane & 7) * 4 < feats ? __ldcs(reinterpret_cast<const float4 *>(q + t * ld))
+                                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+}
+// Through the staging buffer to the accumulator's order (tmem_ld_16x16, both halves).
+__device__ __forceinline__ void rows_to_frag(uint32_t stage, const float4 (&w)[4], int lane, float (&v)[2][8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(
+                     stage + static_cast<uint32_t>((i * 4 + (lane >> 3)) * kFPitch + (lane & 7) * 16)),
+                 "f"(w[i].x), "f"(w[i].y), "f"(w[i].z), "f"(w[i].w)
+                 : "memory");
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int t = (lane & 3) * 2 + (j & 1) + (j >> 2) * 8, f = h * 16 + (lane >> 2) + ((j >> 1) & 1) * 8;
+      asm volatile("ld.shared.f32 %0, [%1];"
+                   : "=f"(v[h][j])
+                   : "r"(stage + static_cast<uint32_t>(t * kFPitch + f * 4))
+                   : "memory");
+    }
+  __syncwarp();
+}
+
+// Epilogue of one warp over tokens (not the weight gradients): acc[chunk][half]
+// holds 16 columns from col0 + 16 chunk of 16 rows from row0 (+ 16).
 template <FfnEpi EPI>
-__device__ __forceinline__ void ffn_epilogue(const FfnGemm &p, const float (&acc)[128], int row0, int col0, int ncols,
-                                             int lane) {
+__device__ __forceinline__ void ffn_epilogue(const FfnGemm &p, const float (&acc)[8][2][8], int row0, int col0,
+                                             int ncols, uint32_t stage, int lane) {
   const int limit = min(ncols, p.cols - col0);  // valid columns
+  if (limit <= 0 || row0 >= p.rows) return;
   if constexpr (EPI == kGateUp) {
-    // row0: first of the warp's 16 features; lanes 0-15 hold their gate values, 16-31 their up values
-    const int f = row0 + (lane & 15);
-    const bool is_gate = lane < 16, ok = f < p.rows;
-    __nv_bfloat16 *act = static_cast<__nv_bfloat16 *>(p.out) + static_cast<int64_t>(col0) * p.ldo + f;
-    float *gu = p.gu ? p.gu + static_cast<int64_t>(col0) * 2 * p.rows + (is_gate ? 0 : p.rows) + f : nullptr;
+    // half 0: gate values of the warp's 16 features from row0, half 1: their up values
+    const RowsOut act{static_cast<__nv_bfloat16 *>(p.out) + static_cast<int64_t>(col0) * p.ldo + row0, p.ldo, limit,
+                      p.rows - row0, true};
+    const int64_t two = 2 * static_cast<int64_t>(p.rows);
+    float *gu = p.gu ? p.gu + col0 * two + row0 + (lane >> 2) : nullptr;
 #pragma unroll
-    for (int c = 0; c < 128; c += 32) {
-      if (c >= limit) break;
-      // the gate lane finishes columns c..c+15, the up lane c+16..c+31
+    for (int c = 0; c < 8; ++c) {
+      if (c * 16 >= limit) break;
+      float a[8];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float mine = is_gate ? acc[c + j] : acc[c + 16 + j];
-        const float other = __shfl_xor_sync(0xffffffffu, is_gate ? acc[c + 16 + j] : acc[c + j], 16);
-        const int t = c + (is_gate ? j : 16 + j);
-        const float g = is_gate ? mine : other, u = is_gate ? other : mine;
-        if (ok && t < limit) act[t * p.ldo] = __float2bfloat16_rn(silu_mul(g, u));
-      }
+      for (int j = 0; j < 8; ++j) a[j] = silu_mul(acc[c][0][j], acc[c][1][j]);
+      store_rows16(stage, a, c * 16, act, lane);
       if (gu) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (ok && c + j < limit) gu[static_cast<int64_t>(c + j) * 2 * p.rows] = acc[c + j];
+        for (int j = 0; j < 8; ++j) {
+          const int t = c * 16 + (lane & 3) * 2 + (j & 1) + (j >> 2) * 8;
+          if (t < limit) {
+            float *o = gu + t * two + ((j >> 1) & 1) * 8;
+            __stcs(o, acc[c][0][j]);
+            __stcs(o + p.rows, acc[c][1][j]);
+          }
+        }
       }
     }
   } else if constexpr (EPI == kStore) {
-    const int f = row0 + lane;
-    if (f >= p.rows || limit <= 0) return;
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + static_cast<int64_t>(col0) * p.ldo + f;
-    if (p.addend) {
-      // the next 16 columns' addends are loaded while these are stored; columns
-      // past the last token load the last one's (no branch between the loads)
-      const __nv_bfloat16 *a = p.addend + static_cast<int64_t>(col0) * p.ld_add + f;
-      __nv_bfloat16 add[2][16];
+    const RowsOut out{static_cast<__nv_bfloat16 *>(p.out) + static_cast<int64_t>(col0) * p.ldo + row0, p.ldo, limit,
+                      p.rows - row0, true};
+    const RowsOut add{const_cast<__nv_bfloat16 *>(p.addend) + static_cast<int64_t>(col0) * p.ld_add + row0, p.ld_add,
+                      limit, p.rows - row0, true};
 #pragma unroll
-      for (int j = 0; j < 16; ++j) add[0][j] = a[min(j, limit - 1) * p.ld_add];
+    for (int c = 0; c < 8; ++c) {
+      if (c * 16 >= limit) break;
+      uint32_t v[2][8];
 #pragma unroll
-      for (int c = 0; c < 128; c += 16) {
-        if (c >= limit) break;
-        if (c + 16 < limit) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) add[(c / 16 + 1) & 1][j] = a[min(c + 16 + j, limit - 1) * p.ld_add];
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (c + j < limit)
-            o[(c + j) * p.ldo] = __float2bfloat16_rn(__fadd_rn(acc[c + j], __bfloat162float(add[(c / 16) & 1][j])));
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 128; ++c)
-        if (c < limit) o[c * p.ldo] = __float2bfloat16_rn(acc[c]);
+      for (int j = 0; j < 16; ++j) v[j / 8][j % 8] = __float_as_uint(acc[c][j / 8][j % 8]);
+      store_rows32(stage, v, c * 16, out, p.addend ? &add : nullptr, lane);
     }
   } else if constexpr (EPI == kDact) {
-    const int f = row0 + lane;
-    if (f >= p.rows || limit <= 0) return;
     const int64_t two = 2 * static_cast<int64_t>(p.rows);
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + col0 * two + f;
-    const float *gu = p.gu + col0 * two + f;
-    float g[2][16], u[2][16];
-    auto load = [&](int c, float (&gv)[16], float (&uv)[16]) {
+    const int feats = p.rows - row0;
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + col0 * two + row0;
+    const RowsOut dg{o, two, limit, feats, true}, du{o + p.rows, two, limit, feats, true};
+    const float *gu = p.gu + col0 * two + row0;
+    // the next chunk's projections are loaded while this one's gradients are stored
+    float4 gw[4], uw[4];
+    load_rows_f32(gu, two, 0, limit, feats, lane, gw);
+    load_rows_f32(gu + p.rows, two, 0, limit, feats, lane, uw);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (c * 16 >= limit) break;
+      float g[2][8], u[2][8];
+      rows_to_frag(stage, gw, lane, g);
+      rows_to_frag(stage, uw, lane, u);
+      if ((c + 1) * 16 < limit) {
+        load_rows_f32(gu, two, (c + 1) * 16, limit, feats, lane, gw);
+        load_rows_f32(gu + p.rows, two, (c + 1) * 16, limit, feats, lane, uw);
+      }
+      uint32_t a[2][8], b[2][8];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const float *at = gu + min(c + j, limit - 1) * two;
-        gv[j] = __ldcs(at);
-        uv[j] = __ldcs(at + p.rows);
+        const int h = j / 8, i = j % 8;
+        a[h][i] = __float_as_uint(dgate(acc[c][h][i], g[h][i], u[h][i]));
+        b[h][i] = __float_as_uint(dup(acc[c][h][i], g[h][i]));
       }
-    };
-    load(0, g[0], u[0]);
-#pragma unroll
-    for (int c = 0; c < 128; c += 16) {
-      if (c >= limit) break;
-      if (c + 16 < limit) load(c + 16, g[(c / 16 + 1) & 1], u[(c / 16 + 1) & 1]);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float gv = g[(c / 16) & 1][j], uv = u[(c / 16) & 1][j];
-        const float d = acc[c + j];
-        if (c + j < limit) {
-          o[(c + j) * two] = __float2bfloat16_rn(dgate(d, gv, uv));
-          o[(c + j) * two + p.rows] = __float2bfloat16_rn(dup(d, gv));
-        }
-      }
+      store_rows32(stage, a, c * 16, dg, nullptr, lane);
+      store_rows32(stage, b, c * 16, du, nullptr, lane);
     }
-  } else {
-    const int r = row0 + lane;
-    if (r >= p.rows) return;
-    const int64_t at = static_cast<int64_t>(r) * p.ldo + col0;
-    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+  }
+}
+
+// Epilogue of one warp of a weight gradient: acc[c] = D[row, col0 + c], row = row0 + lane.
+__device__ __forceinline__ void ffn_wgrad_epilogue(const FfnGemm &p, const float (&acc)[128], int row0, int col0,
+                                                   int ncols, int lane) {
+  const int limit = min(ncols, p.cols - col0), r = row0 + lane;
+  if (r >= p.rows) return;
+  const int64_t at = static_cast<int64_t>(r) * p.ldo + col0;
+  const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll
-    for (int c = 0; c < 128; c += 16) {  // result columns come in multiples of 16
-      if (c >= limit) break;
-      if (p.mode == kGradBf16) {
+  for (int c = 0; c < 128; c += 16) {  // result columns come in multiples of 16
+    if (c >= limit) break;
+    if (p.mode == kGradBf16) {
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = pack_bf16(acc[c + 2 * j], acc[c + 2 * j + 1]);
+      store_32b(static_cast<__nv_bfloat16 *>(p.out) + at + c, v, wide);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 16; h += 8) {
+        float *o = static_cast<float *>(p.out) + at + c + h;
         uint32_t v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = pack_bf16(acc[c + 2 * j], acc[c + 2 * j + 1]);
-        store_32b(static_cast<__nv_bfloat16 *>(p.out) + at + c, v, wide);
-      } else {
-#pragma unroll
-        for (int h = 0; h < 16; h += 8) {
-          float *o = static_cast<float *>(p.out) + at + c + h;
-          uint32_t v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            v[j] = __float_as_uint(p.mode == kGradF32Accumulate ? __fadd_rn(o[j], acc[c + h + j]) : acc[c + h + j]);
-          store_32b(o, v, wide);
-        }
+        for (int j = 0; j < 8; ++j)
+          v[j] = __float_as_uint(p.mode == kGradF32Accumulate ? __fadd_rn(o[j], acc[c + h + j]) : acc[c + h + j]);
+        store_32b(o, v, wide);
       }
     }
   }
@@ -372,30 +404,39 @@ __global__ void __launch_bounds__(kFThreads, 1)
     // -------------------------------------------------------- epilogue --
     const int q = warp & 3, h = (warp - 4) >> 2;
     const int ncols = prm.n / 2;  // columns of this warp: half h of the tile
+    const uint32_t staging = smem_u32(tiles + kFStages * kFStageBytes + 256 + (warp - 4) * kFStaging);
     int buf = 0;
     uint32_t buf_phase = 0;
     bool ok = true;
     for (int tile = unit0; tile < total && ok; tile += nunits) {
-      float acc[128];
+      // the sums of the slices, in the order that the epilogue wants them
+      float acc[8][2][8];
 #pragma unroll
-      for (int c = 0; c < 128; ++c) acc[c] = 0.0f;
+      for (int c = 0; c < 128; ++c) acc[c / 16][c / 8 % 2][c % 8] = 0.0f;
       for (int kb0 = 0; kb0 < prm.nkb; kb0 += prm.slice_kb) {
-        // one lane polls: 256 polling threads slow the MMA thread's own waits
-        int landed = 1;
-        if (lane == 0) landed = wait(smem_u32(&tfull[buf]), buf_phase, abort_flag) ? 1 : 0;
-        ok = __shfl_sync(0xffffffffu, landed, 0) != 0;
+        ok = __all_sync(0xffffffffu, wait(smem_u32(&tfull[buf]), buf_phase, abort_flag) ? 1 : 0) != 0;
         if (!ok) break;
         tc_fence_after();
         const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                            static_cast<uint32_t>(buf * kFAccCols + h * ncols);
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          if (c < ncols) {
-            uint32_t d[16];
-            tmem_ld16(t + c, d);
-            tmem_ld_wait();
+        for (int c = 0; c < 8; ++c) {
+          if (c * 16 < ncols) {
+            uint32_t d[2][8];
+            if (EPI == kWgrad) {
+              uint32_t w[16];
+              tmem_ld16(t + c * 16, w);
+              tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[c + j] = __fadd_rn(acc[c + j], __uint_as_float(d[j]));
+              for (int j = 0; j < 16; ++j) d[j / 8][j % 8] = w[j];
+            } else {
+              tmem_ld_16x16(t + c * 16, d[0]);
+              tmem_ld_16x16(t + (16u << 16) + c * 16, d[1]);
+              tmem_ld_wait();
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              acc[c][j / 8][j % 8] = __fadd_rn(acc[c][j / 8][j % 8], __uint_as_float(d[j / 8][j % 8]));
           }
         }
         tc_fence_before();
@@ -409,7 +450,14 @@ __global__ void __launch_bounds__(kFThreads, 1)
       if (!ok) break;
       const int row0 = row_of(tile) + static_cast<int>(rank) * (EPI == kGateUp ? kFM / 2 : kFM) +
                        q * (EPI == kGateUp ? 16 : 32);
-      ffn_epilogue<EPI>(prm, acc, row0, col_of(tile) + h * ncols, ncols, lane);
+      if constexpr (EPI == kWgrad) {
+        float flat[128];
+#pragma unroll
+        for (int c = 0; c < 128; ++c) flat[c] = acc[c / 16][c / 8 % 2][c % 8];
+        ffn_wgrad_epilogue(prm, flat, row0, col_of(tile) + h * ncols, ncols, lane);
+      } else {
+        ffn_epilogue<EPI>(prm, acc, row0, col_of(tile) + h * ncols, ncols, staging, lane);
+      }
     }
   }
 
