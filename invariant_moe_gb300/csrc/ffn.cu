@@ -63,6 +63,7 @@ struct FfnGemm {
   int64_t ld_add;
   float *gu;            // kGateUp: written (may be null); kDact: read
   int mode;             // kWgrad: GradMode
+  int parts;            // kWgrad: CTA pairs of a cluster that share a tile's reduction
   int *err;
 };
 
@@ -164,13 +165,16 @@ __device__ __forceinline__ void ffn_epilogue(const FfnGemm &p, const float (&acc
                       p.rows - row0, true};
     const RowsOut add{const_cast<__nv_bfloat16 *>(p.addend) + static_cast<int64_t>(col0) * p.ld_add + row0, p.ld_add,
                       limit, p.rows - row0, true};
+    uint4 aw[2][2] = {};  // the addend of a chunk, loaded while the one before is stored
+    if (p.addend) load_rows32(add, 0, lane, aw[0]);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       if (c * 16 >= limit) break;
+      if (p.addend && (c + 1) * 16 < limit) load_rows32(add, (c + 1) * 16, lane, aw[(c + 1) & 1]);
       uint32_t v[2][8];
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j / 8][j % 8] = __float_as_uint(acc[c][j / 8][j % 8]);
-      store_rows32(stage, v, c * 16, out, p.addend ? &add : nullptr, lane);
+      store_rows32(stage, v, c * 16, out, p.addend ? &add : nullptr, aw[c & 1], lane);
     }
   } else if constexpr (EPI == kDact) {
     const int64_t two = 2 * static_cast<int64_t>(p.rows);
@@ -199,21 +203,23 @@ __device__ __forceinline__ void ffn_epilogue(const FfnGemm &p, const float (&acc
         a[h][i] = __float_as_uint(dgate(acc[c][h][i], g[h][i], u[h][i]));
         b[h][i] = __float_as_uint(dup(acc[c][h][i], g[h][i]));
       }
-      store_rows32(stage, a, c * 16, dg, nullptr, lane);
-      store_rows32(stage, b, c * 16, du, nullptr, lane);
+      const uint4 none[2] = {};
+      store_rows32(stage, a, c * 16, dg, nullptr, none, lane);
+      store_rows32(stage, b, c * 16, du, nullptr, none, lane);
     }
   }
 }
 
 // Epilogue of one warp of a weight gradient: acc[c] = D[row, col0 + c], row = row0 + lane.
-__device__ __forceinline__ void ffn_wgrad_epilogue(const FfnGemm &p, const float (&acc)[128], int row0, int col0,
+template <int COLS>
+__device__ __forceinline__ void ffn_wgrad_epilogue(const FfnGemm &p, const float (&acc)[COLS], int row0, int col0,
                                                    int ncols, int lane) {
   const int limit = min(ncols, p.cols - col0), r = row0 + lane;
   if (r >= p.rows) return;
   const int64_t at = static_cast<int64_t>(r) * p.ldo + col0;
   const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll
-  for (int c = 0; c < 128; c += 16) {  // result columns come in multiples of 16
+  for (int c = 0; c < COLS; c += 16) {  // result columns come in multiples of 16
     if (c >= limit) break;
     if (p.mode == kGradBf16) {
       uint32_t v[8];
@@ -250,7 +256,13 @@ __global__ void __launch_bounds__(kFThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  // rank in the pair; kWgrad: which of the cluster's pairs, and its K steps
+  const uint32_t crank = cluster_ctarank(), rank = crank & 1u, lead = crank & ~1u;
+  const int part = EPI == kWgrad ? static_cast<int>(crank >> 1) : 0;
+  const int k_first = EPI == kWgrad ? prm.nkb * part / prm.parts : 0;
+  const int k_last = EPI == kWgrad ? prm.nkb * (part + 1) / prm.parts : prm.nkb;
+  const int slice_kb = EPI == kWgrad ? k_last - k_first : prm.slice_kb;
+  const uint16_t pair_mask = static_cast<uint16_t>(3u << lead);
   const int unit0 = static_cast<int>(cluster_id_x()), nunits = static_cast<int>(num_clusters_x());
   const int total = prm.m_tiles * prm.n_tiles;
 
@@ -304,13 +316,13 @@ __global__ void __launch_bounds__(kFThreads, 1)
         for (int tile = unit0; tile < total && ok; tile += nunits) {
           const int row = row_of(tile) + static_cast<int>(rank) * (EPI == kGateUp ? kFM / 2 : kFM);
           const int col = col_of(tile) + static_cast<int>(rank) * half;
-          for (int kb = 0; kb < prm.nkb; ++kb) {
+          for (int kb = k_first; kb < k_last; ++kb) {
             if (!wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
               ok = false;
               break;
             }
             const uint32_t st = smem_u32(tiles + stage * kFStageBytes);
-            const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
+            const uint32_t fb = mapa_shared(smem_u32(&full[stage]), lead);
             if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * (kFABytes + b_bytes));
             const int k = kb * kFK;
             if (EPI == kGateUp) {
@@ -357,8 +369,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
         uint32_t phase = 0, buf_phase = 0;
         bool ok = true;
         for (int tile = unit0; tile < total && ok && !*abort_flag; tile += nunits) {
-          for (int kb0 = 0; kb0 < prm.nkb && ok; kb0 += prm.slice_kb) {
-            const int kb1 = min(prm.nkb, kb0 + prm.slice_kb);
+          for (int kb0 = k_first; kb0 < k_last && ok; kb0 += slice_kb) {
+            const int kb1 = min(k_last, kb0 + slice_kb);
             if (!wait(smem_u32(&tempty[buf]), buf_phase ^ 1u, abort_flag)) {
               ok = false;
               break;
@@ -378,14 +390,14 @@ __global__ void __launch_bounds__(kFThreads, 1)
                 const uint64_t bd = B_MN ? sdesc_sw128_mn(b0 + k * 2048, kFSlab) : sdesc_sw128(b0 + k * 32);
                 umma_f16_pair(d, ad, bd, idesc, (kb > kb0 || k) ? 1u : 0u);
               }
-              umma_commit_pair(smem_u32(&empty[stage]), 0x3);
+              umma_commit_pair(smem_u32(&empty[stage]), pair_mask);
               if (++stage == kFStages) {
                 stage = 0;
                 phase ^= 1u;
               }
             }
             if (!ok) break;
-            umma_commit_pair(smem_u32(&tfull[buf]), 0x3);
+            umma_commit_pair(smem_u32(&tfull[buf]), pair_mask);
             if (++buf == 2) {
               buf = 0;
               buf_phase ^= 1u;
@@ -393,12 +405,13 @@ __global__ void __launch_bounds__(kFThreads, 1)
           }
         }
         // every MMA into both CTAs' tensor memory has completed
-        umma_commit_pair(smem_u32(drain), 0x3);
+        umma_commit_pair(smem_u32(drain), pair_mask);
         wait(smem_u32(drain), 0, nullptr);
       } else {
         return;
       }
     }
+    if (EPI == kWgrad && prm.parts > 1) cluster_sync_rest();  // the partial tiles are there (see below)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFRegsMany));
     // -------------------------------------------------------- epilogue --
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       float acc[8][2][8];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c / 16][c / 8 % 2][c % 8] = 0.0f;
-      for (int kb0 = 0; kb0 < prm.nkb; kb0 += prm.slice_kb) {
+      for (int kb0 = k_first; kb0 < k_last; kb0 += slice_kb) {
         ok = __all_sync(0xffffffffu, wait(smem_u32(&tfull[buf]), buf_phase, abort_flag) ? 1 : 0) != 0;
         if (!ok) break;
         tc_fence_after();
@@ -441,7 +454,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[buf]), 0));
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[buf]), lead));
         if (++buf == 2) {
           buf = 0;
           buf_phase ^= 1u;
@@ -454,9 +467,46 @@ __global__ void __launch_bounds__(kFThreads, 1)
         float flat[128];
 #pragma unroll
         for (int c = 0; c < 128; ++c) flat[c] = acc[c / 16][c / 8 % 2][c % 8];
-        ffn_wgrad_epilogue(prm, flat, row0, col_of(tile) + h * ncols, ncols, lane);
+        if (prm.parts == 1) {
+          ffn_wgrad_epilogue(prm, flat, row0, col_of(tile) + h * ncols, ncols, lane);
+        } else {
+          // the partial tile [column][row], over the stages: all of this CTA's
+          // copies and MMAs are done
+          float *to = reinterpret_cast<float *>(tiles) + static_cast<size_t>(h * ncols) * kFM + q * 32 + lane;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c < ncols) to[c * kFM] = flat[c];
+        }
       } else {
         ffn_epilogue<EPI>(prm, acc, row0, col_of(tile) + h * ncols, ncols, staging, lane);
+      }
+    }
+    if constexpr (EPI == kWgrad) {
+      if (prm.parts > 1) {
+        // one tile per cluster: the pairs' partial sums are added in pair order
+        // from +0, each CTA finishing its rows of 1 / parts of the columns
+        cluster_sync_rest();
+        const int share = prm.n / prm.parts / 2;  // columns of this warp: 16, 32 or 64
+        const int c0 = part * (prm.n / prm.parts) + h * share;
+        const uint32_t at = smem_u32(tiles) + static_cast<uint32_t>((c0 * kFM + q * 32 + lane) * 4);
+        float sum[64];
+#pragma unroll
+        for (int c = 0; c < 64; ++c) sum[c] = 0.0f;
+        for (int s = 0; s < prm.parts && ok; ++s) {
+          const uint32_t from = mapa_shared(at, static_cast<uint32_t>(2 * s) + rank);
+#pragma unroll
+          for (int c = 0; c < 64; c += 16) {
+            if (c >= share) break;
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = ld_cluster_f32(from + static_cast<uint32_t>((c + j) * kFM * 4));
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[c + j] = __fadd_rn(sum[c + j], v[j]);
+          }
+        }
+        if (ok)
+          ffn_wgrad_epilogue(prm, sum, row_of(unit0) + static_cast<int>(rank) * kFM + q * 32, col_of(unit0) + c0, share,
+                             lane);
       }
     }
   }
@@ -832,9 +882,14 @@ static bi_status launch_ffn(const CUtensorMap &tmA, const CUtensorMap &tmB, FfnG
     set_error("feed-forward product with %lld tiles", (long long)tiles);
     return BI_ERR_UNSUPPORTED;
   }
-  const int units = static_cast<int>(std::min<int64_t>(max_units[dev], tiles));
-  return launch_chained(kern, dim3(2 * units), dim3(kFThreads), kFSmem, s, 2, tmA, tmB, p);
+  // a tile per cluster where its pairs share the reduction (any number of clusters may wait)
+  const int units = p.parts > 1 ? static_cast<int>(tiles) : static_cast<int>(std::min<int64_t>(max_units[dev], tiles));
+  return launch_chained(kern, dim3(2 * p.parts * units), dim3(kFThreads), kFSmem, s, 2 * p.parts, tmA, tmB, p);
 }
+
+// Fewest K steps of a pair that shares a weight-gradient tile (joining the
+// partial sums costs about as much as 16 of them).
+constexpr int kWgradMinSteps = 16;
 
 static int div_up(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
@@ -863,6 +918,7 @@ static FfnGemm plan(int64_t rows, int64_t cols, int64_t K, int64_t slice, int ti
   p.n_tiles = div_up(cols, p.n);
   p.nkb = div_up(K, kFK);
   p.slice_kb = std::max(1, static_cast<int>(slice / kFK));
+  p.parts = 1;
   return p;
 }
 
@@ -996,6 +1052,9 @@ bi_status launch_ffn_wgrad(Mat a, Mat b, void *dw, int grad_mode, int64_t M, int
   p.out = dw;
   p.ldo = cols;
   p.mode = grad_mode;
+  // few tiles and many tokens: 2 or 4 pairs share a tile's tokens
+  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+  while (p.parts < 4 && tiles * p.parts * 2 <= num_sms() / 2 && p.nkb / (p.parts * 2) >= kWgradMinSteps) p.parts *= 2;
   CUtensorMap ta, tb;
   if (!make_tma_2d_bf16_ld(&ta, a.p, M, rows, a.ld, kFK) || !make_tma_2d_bf16_ld(&tb, b.p, M, cols, b.ld, kFK))
     return BI_ERR_CUDA;

@@ -77,10 +77,13 @@ __device__ __forceinline__ void mx4_epilogue(const Mx4Gemm &p, const uint32_t (&
                       rows_aligned(p.y, p.ldy)};
     const RowsOut add{const_cast<__nv_bfloat16 *>(p.addend) + static_cast<int64_t>(col0) * p.ld_add + row0, p.ld_add,
                       limit, p.N - row0, rows_aligned(p.addend, p.ld_add)};
+    uint4 aw[2][2] = {};  // the addend of a chunk, loaded while the one before is stored
+    if (p.addend) load_rows32(add, 0, lane, aw[0]);
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
       if (c * 16 >= limit) break;
-      store_rows32(stage, v[c], c * 16, out, p.addend ? &add : nullptr, lane);
+      if (p.addend && (c + 1) * 16 < limit) load_rows32(add, (c + 1) * 16, lane, aw[(c + 1) & 1]);
+      store_rows32(stage, v[c], c * 16, out, p.addend ? &add : nullptr, aw[c & 1], lane);
     }
   }
 }

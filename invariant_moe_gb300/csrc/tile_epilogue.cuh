@@ -84,11 +84,24 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint16_t v) {
   asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 
+// The part of 16 tokens x 32 features that a lane of store_rows32 loads of rows
+// to be added (16-byte aligned ones; others are loaded there).
+__device__ __forceinline__ void load_rows32(const RowsOut &add, int t0, int lane, uint4 (&w)[2]) {
+  const int f = (lane & 3) * 8, nf = add.feats - f;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int t = t0 + b * 8 + (lane >> 2);
+    w[b] = make_uint4(0, 0, 0, 0);
+    if (add.vec && t < add.tokens && nf > 0) w[b] = load_part(add.p + t * add.ld + f, nf);
+  }
+}
+
 // 16 tokens (t0..) x 32 features: v[g] holds features 16g..16g+15 as
 // tmem_ld_16x16 leaves them.  `stage`: this warp's buffer.  add (may be null):
-// rows added in fp32 before the rounding, same shape and place as out.
+// rows added in fp32 before the rounding, same shape and place as out, `w` what
+// load_rows32 loaded of them.
 __device__ __forceinline__ void store_rows32(uint32_t stage, const uint32_t (&v)[2][8], int t0, const RowsOut &out,
-                                             const RowsOut *add, int lane) {
+                                             const RowsOut *add, const uint4 (&aw)[2], int lane) {
   // lane's row of the four 8 x 8 matrices of a stmatrix / ldmatrix: token lane % 8, features 8 (lane / 8) ..
   const uint32_t mat = stage + static_cast<uint32_t>((lane & 7) * kStagePitch + (lane >> 3) * 16);
   // lane's 16-byte part of the row-wise accesses: token lane / 4 (and 8 further), features 8 (lane % 4) ..
@@ -98,14 +111,10 @@ __device__ __forceinline__ void store_rows32(uint32_t stage, const uint32_t (&v)
   if (add) {
     if (add->vec) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int t = t0 + b * 8 + (lane >> 2);
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (t < add->tokens && nf > 0) w = load_part(add->p + t * add->ld + f, nf);
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(rowp + b * 8 * kStagePitch), "r"(w.x), "r"(w.y),
-                     "r"(w.z), "r"(w.w)
+      for (int b = 0; b < 2; ++b)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(rowp + b * 8 * kStagePitch), "r"(aw[b].x),
+                     "r"(aw[b].y), "r"(aw[b].z), "r"(aw[b].w)
                      : "memory");
-      }
     } else {  // a lane per feature, a token at a time
       uint16_t w[16];
       const uint16_t *q = reinterpret_cast<const uint16_t *>(add->p) + static_cast<int64_t>(t0) * add->ld + lane;

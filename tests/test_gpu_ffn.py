@@ -55,7 +55,8 @@ def test_forward(cuda, M, H, I, with_addend):
     assert bool(((g - torch.cat((r["g"], r["u"]), 1)).abs() <= eg).all())
 
 
-@pytest.mark.parametrize("M,H,I", SHAPES)
+# few weight tiles and many tokens: a tile's tokens are shared by 2 or 4 CTA pairs
+@pytest.mark.parametrize("M,H,I", SHAPES + [(1023, 272, 144), (2500, 144, 528), (4133, 512, 48)])
 def test_backward(cuda, M, H, I):
     import invariant_moe_gb300 as bm
     x, w13, w2, _, dout = make(M, H, I, 30)
