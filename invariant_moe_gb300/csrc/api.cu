@@ -903,10 +903,8 @@ BI_API bi_status bi_ffn_backward(const bi_bf16 *dout, int64_t lddo, const bi_bf1
     BI_REQUIRE(workspace_bytes >= need, BI_ERR_WORKSPACE, "workspace %zu < %zu bytes", workspace_bytes, need);
     BI_TRY(launch_ffn_dact(mat(dout, lddo), cbf(w2), gu, dgu, M, H, I, s));
   }
-  if (dw2) BI_TRY(launch_ffn_wgrad(mat(dout, lddo), mat(act, I), dw2, grad_mode, M, H, I, s));
-  if (dx) BI_TRY(launch_ffn_dx(dgu, cbf(w13), mbf(dx), lddx, M, H, I, s));
-  if (dw13) BI_TRY(launch_ffn_wgrad(Mat{dgu, 2 * I}, mat(x, ldx), dw13, grad_mode, M, 2 * I, H, s));
-  return BI_OK;
+  const FfnGrads d{mat(dout, lddo), mat(x, ldx), dgu, cbf(act), cbf(w13), mbf(dx), lddx, dw13, dw2, grad_mode};
+  return launch_ffn_grads(d, M, H, I, s);
 }
 
 BI_API bi_status bi_ffn_schedule(int32_t mode, int32_t *previous) {

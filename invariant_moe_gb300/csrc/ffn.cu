@@ -50,7 +50,8 @@ constexpr int kFSmem = 1024 + kFStages * kFStageBytes + 256 + 8 * 16 * 144;  // 
 constexpr int kSliceK = 1024;                  // reduction slice of the recipe
 static_assert(kFSmem <= 227 * 1024, "shared memory");
 
-enum FfnEpi { kGateUp, kStore, kDact, kWgrad };
+// kGrads: up to three problems in one launch, each kStore (dx) or kWgrad.
+enum FfnEpi { kGateUp, kStore, kDact, kWgrad, kGrads };
 
 struct FfnGemm {
   int rows, cols;       // valid rows (A side; features) and columns (B side; tokens) of the result
@@ -64,7 +65,19 @@ struct FfnGemm {
   float *gu;            // kGateUp: written (may be null); kDact: read
   int mode;             // kWgrad: GradMode
   int parts;            // kWgrad: CTA pairs of a cluster that share a tile's reduction
+  int wgrad;            // kGrads: a weight gradient (B is MN-major too), else dx
+};
+
+// The problems of a launch and the tile numbers at which they begin.
+template <int N>
+struct FfnBatch {
+  FfnGemm g[N];
+  int first[N + 1];
   int *err;
+};
+template <int N>
+struct FfnMaps {
+  CUtensorMap a[N], b[N];
 };
 
 // The two projections' gradients from dact = d: one fixed fp32 sequence.
@@ -240,10 +253,16 @@ __device__ __forceinline__ void ffn_wgrad_epilogue(const FfnGemm &p, const float
   }
 }
 
+// Columns that an epilogue warp finishes of a weight-gradient tile of n columns
+// shared by `parts` pairs: a multiple of 16, at most 64 for two pairs or more.
+__host__ __device__ constexpr int wgrad_share(int n, int parts) { return (n + 32 * parts - 1) / (32 * parts) * 16; }
+
 template <FfnEpi EPI, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kFThreads, 1)
-    ffn_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ FfnGemm prm) {
+    ffn_gemm_kernel(const __grid_constant__ FfnMaps<EPI == kGrads ? 3 : 1> maps,
+                    const __grid_constant__ FfnBatch<EPI == kGrads ? 3 : 1> batch) {
+  constexpr int kProblems = EPI == kGrads ? 3 : 1;
+  const FfnGemm &one = batch.g[0];  // the only problem, where there is one
   extern __shared__ uint8_t smem_raw[];
   uint8_t *tiles = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -259,12 +278,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
   // rank in the pair; kWgrad: which of the cluster's pairs, and its K steps
   const uint32_t crank = cluster_ctarank(), rank = crank & 1u, lead = crank & ~1u;
   const int part = EPI == kWgrad ? static_cast<int>(crank >> 1) : 0;
-  const int k_first = EPI == kWgrad ? prm.nkb * part / prm.parts : 0;
-  const int k_last = EPI == kWgrad ? prm.nkb * (part + 1) / prm.parts : prm.nkb;
-  const int slice_kb = EPI == kWgrad ? k_last - k_first : prm.slice_kb;
   const uint16_t pair_mask = static_cast<uint16_t>(3u << lead);
   const int unit0 = static_cast<int>(cluster_id_x()), nunits = static_cast<int>(num_clusters_x());
-  const int total = prm.m_tiles * prm.n_tiles;
+  const int total = batch.first[kProblems];
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kFStages; ++s) {
@@ -278,8 +294,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
+    for (int i = 0; i < kProblems; ++i) {
+      if (i > 0 && batch.first[i + 1] == batch.first[i]) continue;
+      tma_prefetch_desc(&maps.a[i]);
+      tma_prefetch_desc(&maps.b[i]);
+    }
   }
   if (warp == 2) {
     if (lane == 0) *tmem_slot = 0u;
@@ -294,10 +313,24 @@ __global__ void __launch_bounds__(kFThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   griddep_wait();
 
-  auto wait = [&](uint32_t bar, uint32_t parity, volatile int *ab) { return mbar_wait_cl(bar, parity, ab, prm.err); };
-  // tokens fastest: the tiles of a row block follow one another and share its A in L2
-  auto row_of = [&](int tile) { return (tile / prm.n_tiles) * (EPI == kGateUp ? kFM : 2 * kFM); };
-  auto col_of = [&](int tile) { return (tile % prm.n_tiles) * prm.n; };
+  auto wait = [&](uint32_t bar, uint32_t parity, volatile int *ab) { return mbar_wait_cl(bar, parity, ab, batch.err); };
+  // A tile: its problem, first row and column (of the pair), K steps and slices.
+  // Columns fastest: the tiles of a row block follow one another and share its A in L2.
+  struct Tile {
+    int i, row, col, k_first, k_last, slice_kb;
+  };
+  auto tile_at = [&](int tile) {
+    Tile t;
+    t.i = kProblems > 1 ? (tile >= batch.first[1]) + (tile >= batch.first[2]) : 0;
+    const FfnGemm &g = batch.g[t.i];
+    const int local = tile - batch.first[t.i];
+    t.row = local / g.n_tiles * (EPI == kGateUp ? kFM : 2 * kFM);
+    t.col = local % g.n_tiles * g.n;
+    t.k_first = EPI == kWgrad ? g.nkb * part / g.parts : 0;
+    t.k_last = EPI == kWgrad ? g.nkb * (part + 1) / g.parts : g.nkb;
+    t.slice_kb = EPI == kWgrad ? t.k_last - t.k_first : g.slice_kb;
+    return t;
+  };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFRegsFew));
@@ -308,15 +341,19 @@ __global__ void __launch_bounds__(kFThreads, 1)
     if (warp == 0) {
       // ---------------------------------------------------- TMA producer --
       if (elect_one()) {
-        const int half = prm.n / 2;
-        const uint32_t b_bytes = B_MN ? static_cast<uint32_t>((half + 63) / 64 * kFSlab) : static_cast<uint32_t>(half * kFK * 2);
         int stage = 0;
         uint32_t phase = 0, issued_mask = 0, issued_parity = 0;
         bool ok = true;
         for (int tile = unit0; tile < total && ok; tile += nunits) {
-          const int row = row_of(tile) + static_cast<int>(rank) * (EPI == kGateUp ? kFM / 2 : kFM);
-          const int col = col_of(tile) + static_cast<int>(rank) * half;
-          for (int kb = k_first; kb < k_last; ++kb) {
+          const Tile ti = tile_at(tile);
+          const CUtensorMap *tmA = &maps.a[ti.i], *tmB = &maps.b[ti.i];
+          const bool b_mn = EPI == kGrads ? batch.g[ti.i].wgrad != 0 : B_MN;
+          const int half = batch.g[ti.i].n / 2;
+          const uint32_t b_bytes =
+              b_mn ? static_cast<uint32_t>((half + 63) / 64 * kFSlab) : static_cast<uint32_t>(half * kFK * 2);
+          const int row = ti.row + static_cast<int>(rank) * (EPI == kGateUp ? kFM / 2 : kFM);
+          const int col = ti.col + static_cast<int>(rank) * half;
+          for (int kb = ti.k_first; kb < ti.k_last; ++kb) {
             if (!wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
               ok = false;
               break;
@@ -326,18 +363,18 @@ __global__ void __launch_bounds__(kFThreads, 1)
             if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * (kFABytes + b_bytes));
             const int k = kb * kFK;
             if (EPI == kGateUp) {
-              tma_load_4d_pair(st, &tmA, fb, k, 0, 0, row / 16);
+              tma_load_4d_pair(st, tmA, fb, k, 0, 0, row / 16);
             } else if (A_MN) {
-              tma_load_2d_pair(st, &tmA, fb, row, k);
-              tma_load_2d_pair(st + kFSlab, &tmA, fb, row + 64, k);
+              tma_load_2d_pair(st, tmA, fb, row, k);
+              tma_load_2d_pair(st + kFSlab, tmA, fb, row + 64, k);
             } else {
-              tma_load_2d_pair(st, &tmA, fb, k, row);
+              tma_load_2d_pair(st, tmA, fb, k, row);
             }
-            if (B_MN) {
-              tma_load_2d_pair(st + kFABytes, &tmB, fb, col, k);
-              if (half > 64) tma_load_2d_pair(st + kFABytes + kFSlab, &tmB, fb, col + 64, k);
+            if (b_mn) {
+              tma_load_2d_pair(st + kFABytes, tmB, fb, col, k);
+              if (half > 64) tma_load_2d_pair(st + kFABytes + kFSlab, tmB, fb, col + 64, k);
             } else {
-              tma_load_2d_pair(st + kFABytes, &tmB, fb, k, col);
+              tma_load_2d_pair(st + kFABytes, tmB, fb, k, col);
             }
             issued_mask |= 1u << stage;
             issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
@@ -364,13 +401,16 @@ __global__ void __launch_bounds__(kFThreads, 1)
     } else if (warp == 1) {
       // ------------------------------------------------------ MMA issuer --
       if (rank == 0 && elect_one()) {
-        const uint32_t idesc = idesc_bf16_f32(2 * kFM, prm.n) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
         int stage = 0, buf = 0;
         uint32_t phase = 0, buf_phase = 0;
         bool ok = true;
         for (int tile = unit0; tile < total && ok && !*abort_flag; tile += nunits) {
-          for (int kb0 = k_first; kb0 < k_last && ok; kb0 += slice_kb) {
-            const int kb1 = min(k_last, kb0 + slice_kb);
+          const Tile ti = tile_at(tile);
+          const bool b_mn = EPI == kGrads ? batch.g[ti.i].wgrad != 0 : B_MN;
+          const uint32_t idesc =
+              idesc_bf16_f32(2 * kFM, batch.g[ti.i].n) | (A_MN ? kIdescAMn : 0u) | (b_mn ? kIdescBMn : 0u);
+          for (int kb0 = ti.k_first; kb0 < ti.k_last && ok; kb0 += ti.slice_kb) {
+            const int kb1 = min(ti.k_last, kb0 + ti.slice_kb);
             if (!wait(smem_u32(&tempty[buf]), buf_phase ^ 1u, abort_flag)) {
               ok = false;
               break;
@@ -387,7 +427,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
 #pragma unroll
               for (int k = 0; k < kFK / 16; ++k) {
                 const uint64_t ad = A_MN ? sdesc_sw128_mn(a0 + k * 2048, kFSlab) : sdesc_sw128(a0 + k * 32);
-                const uint64_t bd = B_MN ? sdesc_sw128_mn(b0 + k * 2048, kFSlab) : sdesc_sw128(b0 + k * 32);
+                const uint64_t bd = b_mn ? sdesc_sw128_mn(b0 + k * 2048, kFSlab) : sdesc_sw128(b0 + k * 32);
                 umma_f16_pair(d, ad, bd, idesc, (kb > kb0 || k) ? 1u : 0u);
               }
               umma_commit_pair(smem_u32(&empty[stage]), pair_mask);
@@ -411,22 +451,25 @@ __global__ void __launch_bounds__(kFThreads, 1)
         return;
       }
     }
-    if (EPI == kWgrad && prm.parts > 1) cluster_sync_rest();  // the partial tiles are there (see below)
+    if (EPI == kWgrad && one.parts > 1) cluster_sync_rest();  // the partial tiles are there (see below)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFRegsMany));
     // -------------------------------------------------------- epilogue --
     const int q = warp & 3, h = (warp - 4) >> 2;
-    const int ncols = prm.n / 2;  // columns of this warp: half h of the tile
     const uint32_t staging = smem_u32(tiles + kFStages * kFStageBytes + 256 + (warp - 4) * kFStaging);
     int buf = 0;
     uint32_t buf_phase = 0;
     bool ok = true;
     for (int tile = unit0; tile < total && ok; tile += nunits) {
+      const Tile ti = tile_at(tile);
+      const FfnGemm &prm = batch.g[ti.i];
+      const bool wgrad = EPI == kGrads ? prm.wgrad != 0 : EPI == kWgrad;
+      const int ncols = prm.n / 2;  // columns of this warp: half h of the tile
       // the sums of the slices, in the order that the epilogue wants them
       float acc[8][2][8];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c / 16][c / 8 % 2][c % 8] = 0.0f;
-      for (int kb0 = k_first; kb0 < k_last; kb0 += slice_kb) {
+      for (int kb0 = ti.k_first; kb0 < ti.k_last; kb0 += ti.slice_kb) {
         ok = __all_sync(0xffffffffu, wait(smem_u32(&tfull[buf]), buf_phase, abort_flag) ? 1 : 0) != 0;
         if (!ok) break;
         tc_fence_after();
@@ -436,7 +479,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         for (int c = 0; c < 8; ++c) {
           if (c * 16 < ncols) {
             uint32_t d[2][8];
-            if (EPI == kWgrad) {
+            if (wgrad) {
               uint32_t w[16];
               tmem_ld16(t + c * 16, w);
               tmem_ld_wait();
@@ -461,42 +504,46 @@ __global__ void __launch_bounds__(kFThreads, 1)
         }
       }
       if (!ok) break;
-      const int row0 = row_of(tile) + static_cast<int>(rank) * (EPI == kGateUp ? kFM / 2 : kFM) +
-                       q * (EPI == kGateUp ? 16 : 32);
-      if constexpr (EPI == kWgrad) {
-        float flat[128];
+      const int row0 = ti.row + static_cast<int>(rank) * (EPI == kGateUp ? kFM / 2 : kFM) + q * (EPI == kGateUp ? 16 : 32);
+      const int col0 = ti.col + h * ncols;
+      if constexpr (EPI == kWgrad || EPI == kGrads) {
+        if (wgrad) {
+          float flat[128];
 #pragma unroll
-        for (int c = 0; c < 128; ++c) flat[c] = acc[c / 16][c / 8 % 2][c % 8];
-        if (prm.parts == 1) {
-          ffn_wgrad_epilogue(prm, flat, row0, col_of(tile) + h * ncols, ncols, lane);
-        } else {
-          // the partial tile [column][row], over the stages: all of this CTA's
-          // copies and MMAs are done
-          float *to = reinterpret_cast<float *>(tiles) + static_cast<size_t>(h * ncols) * kFM + q * 32 + lane;
+          for (int c = 0; c < 128; ++c) flat[c] = acc[c / 16][c / 8 % 2][c % 8];
+          if (EPI == kGrads || prm.parts == 1) {
+            ffn_wgrad_epilogue(prm, flat, row0, col0, ncols, lane);
+          } else {
+            // the partial tile [column][row], over the stages: all of this CTA's
+            // copies and MMAs are done
+            float *to = reinterpret_cast<float *>(tiles) + static_cast<size_t>(h * ncols) * kFM + q * 32 + lane;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c < ncols) to[c * kFM] = flat[c];
+            for (int c = 0; c < 128; ++c)
+              if (c < ncols) to[c * kFM] = flat[c];
+          }
         }
-      } else {
-        ffn_epilogue<EPI>(prm, acc, row0, col_of(tile) + h * ncols, ncols, staging, lane);
+      }
+      if constexpr (EPI != kWgrad) {
+        if (!wgrad) ffn_epilogue<EPI == kGrads ? kStore : EPI>(prm, acc, row0, col0, ncols, staging, lane);
       }
     }
     if constexpr (EPI == kWgrad) {
-      if (prm.parts > 1) {
+      if (one.parts > 1) {
         // one tile per cluster: the pairs' partial sums are added in pair order
         // from +0, each CTA finishing its rows of 1 / parts of the columns
         cluster_sync_rest();
-        const int share = prm.n / prm.parts / 2;  // columns of this warp: 16, 32 or 64
-        const int c0 = part * (prm.n / prm.parts) + h * share;
+        const Tile ti = tile_at(unit0);
+        const int share = wgrad_share(one.n, one.parts);  // columns of this warp, at most
+        const int c0 = part * 2 * share + h * share, ncols = min(share, one.n - c0);
         const uint32_t at = smem_u32(tiles) + static_cast<uint32_t>((c0 * kFM + q * 32 + lane) * 4);
         float sum[64];
 #pragma unroll
         for (int c = 0; c < 64; ++c) sum[c] = 0.0f;
-        for (int s = 0; s < prm.parts && ok; ++s) {
+        for (int s = 0; s < one.parts && ok; ++s) {
           const uint32_t from = mapa_shared(at, static_cast<uint32_t>(2 * s) + rank);
 #pragma unroll
           for (int c = 0; c < 64; c += 16) {
-            if (c >= share) break;
+            if (c >= ncols) break;
             float v[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = ld_cluster_f32(from + static_cast<uint32_t>((c + j) * kFM * 4));
@@ -504,9 +551,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
             for (int j = 0; j < 16; ++j) sum[c + j] = __fadd_rn(sum[c + j], v[j]);
           }
         }
-        if (ok)
-          ffn_wgrad_epilogue(prm, sum, row_of(unit0) + static_cast<int>(rank) * kFM + q * 32, col_of(unit0) + c0, share,
-                             lane);
+        if (ok && ncols > 0)
+          ffn_wgrad_epilogue(one, sum, ti.row + static_cast<int>(rank) * kFM + q * 32, ti.col + c0, ncols, lane);
       }
     }
   }
@@ -557,6 +603,7 @@ struct FfnSplit {
   int stages, stage_bytes, b_off;
   int share;              // elements that a CTA of the cluster finishes
   int early;              // A may be read before the predecessor has finished
+  int *err;
 };
 
 // What an element's epilogue reads besides its sums, loaded apart from its use.
@@ -669,7 +716,7 @@ __global__ void __launch_bounds__(kPThreads)
       int s = 0, i = 0;
       uint32_t phase = 1;
       for (; i < steps; ++i) {
-        if (i >= sp.stages && !mbar_wait(empty0 + s * 8, phase, abort_flag, prm.err)) break;
+        if (i >= sp.stages && !mbar_wait(empty0 + s * 8, phase, abort_flag, sp.err)) break;
         const uint32_t st = tiles0 + static_cast<uint32_t>(s * sp.stage_bytes), fb = full0 + s * 8;
         mbar_arrive_expect_tx(fb, bytes);
 #pragma unroll
@@ -691,7 +738,7 @@ __global__ void __launch_bounds__(kPThreads)
       }
       if (*abort_flag) {  // every copy this CTA started lands before it exits
         for (int j = max(0, i - sp.stages); j < i; ++j)
-          mbar_wait(full0 + j % sp.stages * 8, j / sp.stages & 1, nullptr, prm.err);
+          mbar_wait(full0 + j % sp.stages * 8, j / sp.stages & 1, nullptr, sp.err);
       }
       if (sp.early) griddep_wait();
     } else {
@@ -708,7 +755,7 @@ __global__ void __launch_bounds__(kPThreads)
       const uint32_t b_sub = static_cast<uint32_t>(prm.n * kFK * 2) / 16;
       uint32_t at = 0, stage = 0, phase = 0;
       for (int i = 0; i < steps; ++i) {
-        if (!mbar_wait(full0 + stage * 8, phase, abort_flag, prm.err)) break;
+        if (!mbar_wait(full0 + stage * 8, phase, abort_flag, sp.err)) break;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < kPK / 16; ++k)
@@ -726,7 +773,7 @@ __global__ void __launch_bounds__(kPThreads)
       // Only this thread polls for the accumulator; the rest of the CTA sleeps
       // at the block barrier below.  After an abort the MMAs that were issued
       // still complete.
-      if (!mbar_wait(smem_u32(done), 0, nullptr, prm.err)) *abort_flag = 1;
+      if (!mbar_wait(smem_u32(done), 0, nullptr, sp.err)) *abort_flag = 1;
       tc_fence_before();
       griddep_wait();
     } else {
@@ -739,7 +786,7 @@ __global__ void __launch_bounds__(kPThreads)
       int s = 0;
       uint32_t phase = 1;
       for (int i = 0; i < steps; ++i) {
-        if (i >= sp.stages && !mbar_wait(empty0 + s * 8, phase, abort_flag, prm.err)) break;
+        if (i >= sp.stages && !mbar_wait(empty0 + s * 8, phase, abort_flag, sp.err)) break;
         const uint32_t st = tiles0 + static_cast<uint32_t>(s * sp.stage_bytes + sp.b_off);
         tma_load_2d(st, &tmB, full0 + s * 8, k0 + i * kPK, col);
         tma_load_2d(st + static_cast<uint32_t>(prm.n * kFK * 2), &tmB, full0 + s * 8, k0 + i * kPK + kFK, col);
@@ -839,8 +886,8 @@ __global__ void __launch_bounds__(kPThreads)
 }
 
 // ------------------------------------------------------------------- host --
-template <FfnEpi EPI, bool A_MN, bool B_MN>
-static bi_status launch_ffn(const CUtensorMap &tmA, const CUtensorMap &tmB, FfnGemm p, cudaStream_t s) {
+template <FfnEpi EPI, bool A_MN, bool B_MN, int N>
+static bi_status launch_ffn(const FfnMaps<N> &maps, FfnBatch<N> p, cudaStream_t s) {
   static std::mutex mu;
   static int max_units[64] = {};  // CTA pairs resident at once, per device
   static ContextSetup setup;      // the shared-memory attribute is per context
@@ -877,48 +924,65 @@ static bi_status launch_ffn(const CUtensorMap &tmA, const CUtensorMap &tmB, FfnG
     }
   }
   p.err = device_error_word();
-  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-  if (tiles > (int64_t(1) << 30)) {
-    set_error("feed-forward product with %lld tiles", (long long)tiles);
-    return BI_ERR_UNSUPPORTED;
+  int64_t tiles = 0;
+  p.first[0] = 0;
+  for (int i = 0; i < N; ++i) {
+    tiles += static_cast<int64_t>(p.g[i].m_tiles) * p.g[i].n_tiles;
+    if (tiles > (int64_t(1) << 30)) {
+      set_error("feed-forward product with more than 2^30 tiles");
+      return BI_ERR_UNSUPPORTED;
+    }
+    p.first[i + 1] = static_cast<int>(tiles);
   }
   // a tile per cluster where its pairs share the reduction (any number of clusters may wait)
-  const int units = p.parts > 1 ? static_cast<int>(tiles) : static_cast<int>(std::min<int64_t>(max_units[dev], tiles));
-  return launch_chained(kern, dim3(2 * p.parts * units), dim3(kFThreads), kFSmem, s, 2 * p.parts, tmA, tmB, p);
+  const int parts = EPI == kWgrad ? p.g[0].parts : 1;
+  const int units = static_cast<int>(parts > 1 ? tiles : std::min<int64_t>(max_units[dev], tiles));
+  return launch_chained(kern, dim3(2 * parts * units), dim3(kFThreads), kFSmem, s, 2 * parts, maps, p);
 }
 
-// Fewest K steps of a pair that shares a weight-gradient tile (joining the
-// partial sums costs about as much as 16 of them).
-constexpr int kWgradMinSteps = 16;
+// In tile_cost's unit (2 cycles): a kernel boundary, and joining the partial sums
+// of pairs that share a weight-gradient tile; and the fewest K steps of such a pair.
+constexpr int64_t kLaunchCost = 2500, kJoinCost = 2500;
+constexpr int kWgradMinSteps = 8;
 
 static int div_up(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-// rows x cols result, reduction length K in slices of `slice`.  Columns of a
-// tile: the multiple of 32 up to 256 with the least time by a simple model:
-// waves of tiles over the CTA pairs, each as long as its columns plus a
-// constant (what a tile costs besides its MMAs, and that narrow MMAs do not
-// run faster than about 64 columns' time).  MN-major B (n_step 128): only whole
-// slabs per CTA, as a part of a slab costs a whole one's copy (dW2 of 8191
-// tokens, H=4096, I=2048: 104 us with 160 columns, 85 us with 256).
-static FfnGemm plan(int64_t rows, int64_t cols, int64_t K, int64_t slice, int tile_rows, int n_step) {
+// What a tile of n columns costs a CTA pair, in MMA columns per K step (256
+// columns take 512 cycles): its MMAs or its copies, whichever is longer (an SM
+// takes 64 bytes a cycle: 16 KB of A and 64 n bytes of B per K step), and a
+// constant for the tile.
+static int64_t tile_cost(int n, int nkb) { return static_cast<int64_t>(nkb) * std::max(n, 128 + n / 2) + 2000; }
+
+// rows x cols result, reduction length K in slices of `slice`; n columns a tile.
+static FfnGemm problem(int64_t rows, int64_t cols, int64_t K, int64_t slice, int tile_rows, int n) {
   FfnGemm p{};
   p.rows = static_cast<int>(rows);
   p.cols = static_cast<int>(cols);
   p.m_tiles = div_up(rows, tile_rows);
-  const int64_t pairs = std::max(1, num_sms() / 2);
-  int64_t best = INT64_MAX;
-  for (int n = 256; n >= n_step; n -= n_step) {
-    const int64_t tiles = static_cast<int64_t>(p.m_tiles) * div_up(cols, n);
-    const int64_t cost = (tiles + pairs - 1) / pairs * (std::max(n, 64) + 16);
-    if (cost < best) {
-      best = cost;
-      p.n = n;
-    }
-  }
-  p.n_tiles = div_up(cols, p.n);
+  p.n = n;
+  p.n_tiles = div_up(cols, n);
   p.nkb = div_up(K, kFK);
   p.slice_kb = std::max(1, static_cast<int>(slice / kFK));
   p.parts = 1;
+  return p;
+}
+
+// The same with the columns a tile (a multiple of 32 up to 256) whose waves over
+// the CTA pairs take the least time by tile_cost.  n_step 128 for an MN-major B:
+// only whole slabs per CTA, as a part of a slab costs a whole one's copy (dW2 of
+// 8191 tokens, H=4096, I=2048: 104 us with 160 columns, 85 us with 256).
+static FfnGemm plan(int64_t rows, int64_t cols, int64_t K, int64_t slice, int tile_rows, int n_step) {
+  const int64_t pairs = std::max(1, num_sms() / 2);
+  int64_t best = INT64_MAX;
+  FfnGemm p{};
+  for (int n = 256; n >= n_step; n -= n_step) {
+    const FfnGemm q = problem(rows, cols, K, slice, tile_rows, n);
+    const int64_t cost = (static_cast<int64_t>(q.m_tiles) * q.n_tiles + pairs - 1) / pairs * tile_cost(n, q.nkb);
+    if (cost < best) {
+      best = cost;
+      p = q;
+    }
+  }
   return p;
 }
 
@@ -943,8 +1007,8 @@ static bi_status launch_split(FfnGemm g, int64_t rows, int64_t M, int64_t K, boo
   g.slice_kb = kSliceK / kFK;
   g.cols = static_cast<int>(M);
   g.n = static_cast<int>(std::min<int64_t>(kPMaxN, (M + 15) / 16 * 16));
-  g.err = device_error_word();
   p.g = g;
+  p.err = device_error_word();
   const int slices = div_up(K, kSliceK), token_tiles = div_up(M, g.n);
   // the tallest tiles that still give four fifths of the SMs a CTA
   p.tile_rows = kFM;
@@ -997,9 +1061,10 @@ bi_status launch_ffn_gate_up(Mat x, const __nv_bfloat16 *w13, __nv_bfloat16 *act
     return launch_split<kGateUp, false>(
         p, 2 * I, M, H, false,
         [&](CUtensorMap *a, int r) { return make_tma_inter_bf16(a, w13, I, I, H, r / 32); }, x.p, x.ld, s);
-  CUtensorMap a, b;
-  if (!make_tma_inter_bf16(&a, w13, I, I, H) || !make_tma_2d_bf16_ld(&b, x.p, M, H, x.ld, p.n / 2)) return BI_ERR_CUDA;
-  return launch_ffn<kGateUp, false, false>(a, b, p, s);
+  FfnMaps<1> m;
+  if (!make_tma_inter_bf16(m.a, w13, I, I, H) || !make_tma_2d_bf16_ld(m.b, x.p, M, H, x.ld, p.n / 2))
+    return BI_ERR_CUDA;
+  return launch_ffn<kGateUp, false, false>(m, FfnBatch<1>{{p}, {}, nullptr}, s);
 }
 
 bi_status launch_ffn_down(const __nv_bfloat16 *act, const __nv_bfloat16 *w2, Mat addend, __nv_bfloat16 *out,
@@ -1012,9 +1077,9 @@ bi_status launch_ffn_down(const __nv_bfloat16 *act, const __nv_bfloat16 *w2, Mat
   if (use_split(M, I))  // launched behind launch_ffn_gate_up, which writes no weights: W2 may be read early
     return launch_split<kStore, false>(
         p, H, M, I, true, [&](CUtensorMap *a, int r) { return make_tma_2d_bf16(a, w2, H, I, r); }, act, I, s);
-  CUtensorMap a, b;
-  if (!make_tma_2d_bf16(&a, w2, H, I, kFM) || !make_tma_2d_bf16(&b, act, M, I, p.n / 2)) return BI_ERR_CUDA;
-  return launch_ffn<kStore, false, false>(a, b, p, s);
+  FfnMaps<1> m;
+  if (!make_tma_2d_bf16(m.a, w2, H, I, kFM) || !make_tma_2d_bf16(m.b, act, M, I, p.n / 2)) return BI_ERR_CUDA;
+  return launch_ffn<kStore, false, false>(m, FfnBatch<1>{{p}, {}, nullptr}, s);
 }
 
 bi_status launch_ffn_dact(Mat dout, const __nv_bfloat16 *w2, const float *gu, __nv_bfloat16 *dgu, int64_t M, int64_t H,
@@ -1026,39 +1091,107 @@ bi_status launch_ffn_dact(Mat dout, const __nv_bfloat16 *w2, const float *gu, __
   if (use_split(M, H))
     return launch_split<kDact, true>(
         p, I, M, H, false, [&](CUtensorMap *a, int) { return make_tma_2d_bf16(a, w2, H, I, kFK); }, dout.p, dout.ld, s);
-  CUtensorMap a, b;
-  if (!make_tma_2d_bf16(&a, w2, H, I, kFK) || !make_tma_2d_bf16_ld(&b, dout.p, M, H, dout.ld, p.n / 2))
+  FfnMaps<1> m;
+  if (!make_tma_2d_bf16(m.a, w2, H, I, kFK) || !make_tma_2d_bf16_ld(m.b, dout.p, M, H, dout.ld, p.n / 2))
     return BI_ERR_CUDA;
-  return launch_ffn<kDact, true, false>(a, b, p, s);
+  return launch_ffn<kDact, true, false>(m, FfnBatch<1>{{p}, {}, nullptr}, s);
 }
 
-bi_status launch_ffn_dx(const __nv_bfloat16 *dgu, const __nv_bfloat16 *w13, __nv_bfloat16 *dx, int64_t lddx, int64_t M,
-                        int64_t H, int64_t I, cudaStream_t s) {
-  FfnGemm p = plan(H, M, 2 * I, kSliceK, 2 * kFM, 32);
-  p.out = dx;
-  p.ldo = lddx;
-  if (use_split(M, 2 * I))
-    return launch_split<kStore, true>(
-        p, H, M, 2 * I, false, [&](CUtensorMap *a, int) { return make_tma_2d_bf16(a, w13, 2 * I, H, kFK); }, dgu, 2 * I,
-        s);
-  CUtensorMap a, b;
-  if (!make_tma_2d_bf16(&a, w13, 2 * I, H, kFK) || !make_tma_2d_bf16(&b, dgu, M, 2 * I, p.n / 2)) return BI_ERR_CUDA;
-  return launch_ffn<kStore, true, false>(a, b, p, s);
+// dx alone, for few tokens (the split kernel).
+static bi_status launch_dx_split(const FfnGrads &d, int64_t M, int64_t H, int64_t I, cudaStream_t s) {
+  FfnGemm p = problem(H, M, 2 * I, kSliceK, 2 * kFM, 256);
+  p.out = d.dx;
+  p.ldo = d.lddx;
+  return launch_split<kStore, true>(
+      p, H, M, 2 * I, false, [&](CUtensorMap *a, int) { return make_tma_2d_bf16(a, d.w13, 2 * I, H, kFK); }, d.dgu,
+      2 * I, s);
 }
 
-bi_status launch_ffn_wgrad(Mat a, Mat b, void *dw, int grad_mode, int64_t M, int64_t rows, int64_t cols,
-                           cudaStream_t s) {
-  FfnGemm p = plan(rows, cols, M, (M + kFK - 1) / kFK * kFK, 2 * kFM, 128);
-  p.out = dw;
-  p.ldo = cols;
-  p.mode = grad_mode;
-  // few tiles and many tokens: 2 or 4 pairs share a tile's tokens
-  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-  while (p.parts < 4 && tiles * p.parts * 2 <= num_sms() / 2 && p.nkb / (p.parts * 2) >= kWgradMinSteps) p.parts *= 2;
-  CUtensorMap ta, tb;
-  if (!make_tma_2d_bf16_ld(&ta, a.p, M, rows, a.ld, kFK) || !make_tma_2d_bf16_ld(&tb, b.p, M, cols, b.ld, kFK))
+// A weight gradient alone, its tokens shared by `parts` pairs.
+static bi_status launch_wgrad(FfnGemm p, int parts, Mat a, Mat b, int64_t M, int64_t rows, int64_t cols,
+                              cudaStream_t s) {
+  p.parts = parts;
+  FfnMaps<1> m;
+  if (!make_tma_2d_bf16_ld(m.a, a.p, M, rows, a.ld, kFK) || !make_tma_2d_bf16_ld(m.b, b.p, M, cols, b.ld, kFK))
     return BI_ERR_CUDA;
-  return launch_ffn<kWgrad, true, true>(ta, tb, p, s);
+  return launch_ffn<kWgrad, true, true>(m, FfnBatch<1>{{p}, {}, nullptr}, s);
+}
+
+// The products that need no more than dgu: dW13, dW2 and dx, as asked for.  In
+// one launch, longest tiles first: their tiles fill the CTA pairs together
+// (4096 tokens, H=2048, I=768: 48 + 24 + 128 tiles on 76 pairs; the backward
+// pass 65 us, with a launch each 91 us).  Where the weight gradients have few
+// tiles but many tokens, each has a launch of its own in which clusters of pairs
+// share a tile.
+bi_status launch_ffn_grads(const FfnGrads &d, int64_t M, int64_t H, int64_t I, cudaStream_t s) {
+  const int64_t pairs = std::max(1, num_sms() / 2), all = (M + kFK - 1) / kFK * kFK;
+  const int nkb = div_up(M, kFK);
+  auto wgrad = [&](int64_t rows, int64_t cols, int n, void *out) {
+    FfnGemm p = problem(rows, cols, M, all, 2 * kFM, n);
+    p.out = out;
+    p.ldo = cols;
+    p.mode = d.grad_mode;
+    p.wgrad = 1;
+    return p;
+  };
+  auto tiles_of = [](const FfnGemm &p) { return static_cast<int64_t>(p.m_tiles) * p.n_tiles; };
+  FfnGemm dx = plan(H, M, 2 * I, kSliceK, 2 * kFM, 32);
+  dx.out = d.dx;
+  dx.ldo = d.lddx;
+  // One launch for all, or a launch each with 2 to 4 pairs a tile?  Decided as
+  // if all three were asked for, so that a gradient's bits do not depend on that.
+  const bool dx_fits = use_split(M, 2 * I);  // dx by the split kernel
+  int n_w = 256, parts = 1;
+  {
+    int64_t best = INT64_MAX;
+    for (int n = 256; n >= 128; n -= 128) {
+      const int64_t t13 = tiles_of(wgrad(2 * I, H, n, nullptr)), t2 = tiles_of(wgrad(H, I, n, nullptr));
+      const int64_t tdx = dx_fits ? 0 : tiles_of(dx), c_dx = tile_cost(dx.n, dx.nkb), c_w = tile_cost(n, nkb);
+      // together: the work over the pairs, and half of the longest tile of imbalance
+      int64_t cost = std::max((t13 + t2) * c_w + tdx * c_dx, (std::max(c_w, tdx ? c_dx : 0)) * pairs) / pairs +
+                     std::max(c_w, tdx ? c_dx : 0) / 2;
+      if (cost < best) best = cost, n_w = n, parts = 1;
+      const int64_t dx_alone = tdx ? (tdx + pairs - 1) / pairs * c_dx + kLaunchCost : 0;
+      for (int q = 2; q <= 4 && nkb / q >= kWgradMinSteps && std::max(t13, t2) * q <= pairs; ++q) {
+        cost = 2 * (tile_cost(n, div_up(nkb, q)) + kJoinCost) + kLaunchCost + dx_alone;
+        if (cost < best) best = cost, n_w = n, parts = q;
+      }
+    }
+  }
+  const bool dx_split = d.dx && dx_fits;
+  if (dx_split) {
+    const bi_status st = launch_dx_split(d, M, H, I, s);
+    if (st != BI_OK) return st;
+  }
+  const Mat dgu{d.dgu, 2 * I}, act{d.act, I};
+  if (parts > 1) {
+    bi_status st = BI_OK;
+    if (d.dw13) st = launch_wgrad(wgrad(2 * I, H, n_w, d.dw13), parts, dgu, d.x, M, 2 * I, H, s);
+    if (st == BI_OK && d.dw2) st = launch_wgrad(wgrad(H, I, n_w, d.dw2), parts, d.dout, act, M, H, I, s);
+    if (st != BI_OK) return st;
+  }
+  FfnBatch<3> b{};
+  FfnMaps<3> m;
+  int n = 0;
+  bool ok = true;
+  auto add = [&](const FfnGemm &p, Mat l, Mat r, uint64_t k_l, uint64_t k_r, uint64_t cols_l, uint64_t cols_r,
+                 uint32_t box_r) {
+    b.g[n] = p;
+    ok = ok && make_tma_2d_bf16_ld(&m.a[n], l.p, k_l, cols_l, l.ld, kFK) &&
+         make_tma_2d_bf16_ld(&m.b[n], r.p, k_r, cols_r, r.ld, box_r);
+    ++n;
+  };
+  const bool with_dx = d.dx && !dx_split;
+  const bool dx_first = with_dx && tile_cost(dx.n, dx.nkb) > tile_cost(n_w, nkb);
+  auto add_dx = [&] { add(dx, Mat{d.w13, H}, dgu, 2 * I, M, H, 2 * I, dx.n / 2); };
+  if (dx_first) add_dx();
+  if (parts == 1 && d.dw13) add(wgrad(2 * I, H, n_w, d.dw13), dgu, d.x, M, M, 2 * I, H, kFK);
+  if (parts == 1 && d.dw2) add(wgrad(H, I, n_w, d.dw2), d.dout, act, M, M, H, I, kFK);
+  if (with_dx && !dx_first) add_dx();
+  if (!ok) return BI_ERR_CUDA;
+  if (n == 0) return BI_OK;
+  for (int i = n; i < 3; ++i) m.a[i] = m.a[0], m.b[i] = m.b[0];  // (no tile uses them)
+  return launch_ffn<kGrads, true, false>(m, b, s);
 }
 
 }  // namespace bimoe

@@ -31,12 +31,16 @@ bi_status launch_ffn_down(const __nv_bfloat16 *act, const __nv_bfloat16 *w2, Mat
 // dgu [M, 2I] = the gradient of the two projections, from dact = dout W2
 bi_status launch_ffn_dact(Mat dout, const __nv_bfloat16 *w2, const float *gu, __nv_bfloat16 *dgu, int64_t M, int64_t H,
                           int64_t I, cudaStream_t s);
-// dx [M, H] = dgu W13
-bi_status launch_ffn_dx(const __nv_bfloat16 *dgu, const __nv_bfloat16 *w13, __nv_bfloat16 *dx, int64_t lddx, int64_t M,
-                        int64_t H, int64_t I, cudaStream_t s);
-// dw [rows, cols] = a^T b over M tokens, a [M, rows], b [M, cols]
-bi_status launch_ffn_wgrad(Mat a, Mat b, void *dw, int grad_mode, int64_t M, int64_t rows, int64_t cols,
-                           cudaStream_t s);
+// dx [M, H] = dgu W13, dw13 [2I, H] = dgu^T x, dw2 [H, I] = dout^T act; what is null is not computed
+struct FfnGrads {
+  Mat dout, x;
+  const __nv_bfloat16 *dgu, *act, *w13;
+  __nv_bfloat16 *dx;
+  int64_t lddx;
+  void *dw13, *dw2;
+  int grad_mode;
+};
+bi_status launch_ffn_grads(const FfnGrads &d, int64_t M, int64_t H, int64_t I, cudaStream_t s);
 
 int set_ffn_schedule(int mode);  // bi_ffn_schedule; returns the old mode
 

@@ -77,10 +77,11 @@ def test_backward(cuda, M, H, I):
     assert torch.equal(a13, f13 + f13) and torch.equal(a2, f2 + f2)
 
 
-def test_backward_parts(cuda):
+@pytest.mark.parametrize("M,H,I", [(20, 160, 96), (70, 160, 96), (700, 1040, 720), (3000, 272, 144)])
+def test_backward_parts(cuda, M, H, I):
     """Each gradient alone has the bits it has beside the others."""
     import invariant_moe_gb300 as bm
-    x, w13, w2, _, dout = (t.to(cuda) for t in make(70, 160, 96, 50))
+    x, w13, w2, _, dout = (t.to(cuda) for t in make(M, H, I, 50))
     _, gu, act = bm.bi_ffn_forward_train(x, w13, w2)
     full = bm.bi_ffn_backward(dout, x, w13, w2, gu, act)
     for i in range(3):
