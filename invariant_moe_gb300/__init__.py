@@ -525,10 +525,13 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _fns = {}
 
 
+_current_device = torch._C._cuda_getDevice
+
+
 def _launch(name, device, stream, *args):
     """Calls a stream-ordered entry point on device number ``device``: on
     ``stream``, or on that device's current stream, with the device current."""
-    if device != torch._C._cuda_getDevice():
+    if device != _current_device():
         with torch.cuda.device(device):
             return _launch(name, device, stream, *args)
     f = _fns.get(name)
@@ -550,13 +553,15 @@ def _device_of(t, name):
 
 def _flat(t, dtype, name, device):
     """Address of a contiguous tensor on device number ``device``."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
         return t.data_ptr()
     return _ptr(t, dtype, name, torch.device("cuda", device)).value  # says what is wrong
 
 
 def _rows(t, dtype, name, rows, cols, device):
     """(address, row stride) of a [rows, cols] tensor with unit column stride on device number ``device``."""
+    if t.dtype is dtype and t.get_device() == device and t.shape == (rows, cols) and t.is_contiguous():
+        return t.data_ptr(), cols
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
@@ -565,14 +570,9 @@ def _rows(t, dtype, name, rows, cols, device):
         raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {[rows, cols]}, got {list(t.shape)}")
-    if rows <= 1:
-        if cols > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name} must have unit column stride")
-        return t.data_ptr(), cols
-    ld, unit = t.stride()
-    if unit != 1 and cols > 1:
+    if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride")
-    return t.data_ptr(), ld
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
 
 
 def _check_ffn_shapes(x, w13, w2):
@@ -723,13 +723,14 @@ def mx4_interleave_gate_up(w13):
 
 def _mx4_operand(q, s, name, device):
     """(addresses, rows, K) of a quantised matrix on device number ``device``."""
-    pq, ps = _flat(q, _U8, name + " codes", device), _flat(s, _U8, name + " scales", device)
-    if q.dim() != 2:
-        raise ValueError(f"{name} codes must be [rows, K/2]")
     R, half = q.shape
-    if s.shape != ((R + 127) // 128, (half + 63) // 64, 512):
+    # the common case in one condition; otherwise find out what is wrong
+    if not (q.dtype is _U8 and s.dtype is _U8 and q.get_device() == device and s.get_device() == device
+            and q.is_contiguous() and s.is_contiguous() and s.shape == ((R + 127) >> 7, (half + 63) >> 6, 512)):
+        _flat(q, _U8, name + " codes", device)
+        _flat(s, _U8, name + " scales", device)
         raise ValueError(f"{name} scales must be {list(mx4_scale_shape(R, 2 * half))}, got {list(s.shape)}")
-    return pq, ps, R, 2 * half
+    return q.data_ptr(), s.data_ptr(), R, 2 * half
 
 
 def bi_mx4_quantize(x, q=None, scales=None, stream=None):
