@@ -528,18 +528,13 @@ _fns = {}
 _current_device = torch._C._cuda_getDevice
 
 
-def _launch(name, device, stream, *args):
-    """Calls a stream-ordered entry point on device number ``device``: on
-    ``stream``, or on that device's current stream, with the device current."""
-    if device != _current_device():
-        with torch.cuda.device(device):
-            return _launch(name, device, stream, *args)
-    f = _fns.get(name)
-    if f is None:
-        f = _fns[name] = getattr(load_library(), name)
-    st = f(*args, _raw_stream(device) if stream is None else stream.cuda_stream)
-    if st != BI_OK:
-        raise BimoeError(name, st, load_library().bi_last_error_message().decode())
+def _bind(name):
+    f = _fns[name] = getattr(load_library(), name)
+    return f
+
+
+def _fail(name, status):
+    raise BimoeError(name, status, load_library().bi_last_error_message().decode())
 
 
 def _device_of(t, name):
@@ -610,8 +605,15 @@ def bi_ffn_forward(x, w13, w2, addend=None, out=None, workspace=None, stream=Non
     po, ldo = _rows(out, _BF, "out", M, H, dev)
     if workspace is None:
         workspace = ffn_workspace(M, H, I, x.device)
-    _launch("bi_ffn_forward", dev, stream, px, ldx, _flat(w13, _BF, "w13", dev), _flat(w2, _BF, "w2", dev), pa, lda,
-            po, ldo, M, H, I, _flat(workspace, _U8, "workspace", dev), workspace.numel())
+    if dev != _current_device():  # the call runs with the tensors' device current
+        with torch.cuda.device(dev):
+            return bi_ffn_forward(x, w13, w2, addend, out, workspace, stream)
+    f = _fns.get("bi_ffn_forward") or _bind("bi_ffn_forward")
+    st = f(px, ldx, _flat(w13, _BF, "w13", dev), _flat(w2, _BF, "w2", dev), pa, lda, po, ldo, M, H, I,
+           _flat(workspace, _U8, "workspace", dev), workspace.numel(),
+           _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _fail("bi_ffn_forward", st)
     return out
 
 
@@ -630,8 +632,15 @@ def bi_ffn_forward_train(x, w13, w2, addend=None, out=None, gu=None, act=None, s
         act = torch.empty(M, I, dtype=_BF, device=x.device)
     if gu.shape != (M, 2 * I) or act.shape != (M, I):
         raise ValueError("gu must be [M, 2I] and act [M, I]")
-    _launch("bi_ffn_forward_train", dev, stream, px, ldx, _flat(w13, _BF, "w13", dev), _flat(w2, _BF, "w2", dev), pa,
-            lda, po, ldo, _flat(gu, _F32, "gu", dev), _flat(act, _BF, "act", dev), M, H, I)
+    if dev != _current_device():  # the call runs with the tensors' device current
+        with torch.cuda.device(dev):
+            return bi_ffn_forward_train(x, w13, w2, addend, out, gu, act, stream)
+    f = _fns.get("bi_ffn_forward_train") or _bind("bi_ffn_forward_train")
+    st = f(px, ldx, _flat(w13, _BF, "w13", dev), _flat(w2, _BF, "w2", dev), pa, lda, po, ldo,
+           _flat(gu, _F32, "gu", dev), _flat(act, _BF, "act", dev), M, H, I,
+           _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _fail("bi_ffn_forward_train", st)
     return out, gu, act
 
 
@@ -672,9 +681,16 @@ def bi_ffn_backward(dout, x, w13, w2, gu, act, dx=None, dw13=None, dw2=None, nee
     if workspace is None:
         workspace = ffn_workspace(M, H, I, x.device)
     mode = 0 if wd is _BF else (2 if accumulate else 1)
-    _launch("bi_ffn_backward", dev, stream, pdo, lddo, px, ldx, _flat(w13, _BF, "w13", dev), _flat(w2, _BF, "w2", dev),
-            _flat(gu, _F32, "gu", dev), _flat(act, _BF, "act", dev), pdx, lddx, p13, p2, mode, M, H, I,
-            _flat(workspace, _U8, "workspace", dev), workspace.numel())
+    if dev != _current_device():  # the call runs with the tensors' device current
+        with torch.cuda.device(dev):
+            return bi_ffn_backward(dout, x, w13, w2, gu, act, dx, dw13, dw2, need, accumulate, workspace, stream)
+    f = _fns.get("bi_ffn_backward") or _bind("bi_ffn_backward")
+    st = f(pdo, lddo, px, ldx, _flat(w13, _BF, "w13", dev), _flat(w2, _BF, "w2", dev),
+           _flat(gu, _F32, "gu", dev), _flat(act, _BF, "act", dev), pdx, lddx, p13, p2, mode, M, H, I,
+           _flat(workspace, _U8, "workspace", dev), workspace.numel(),
+           _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _fail("bi_ffn_backward", st)
     return dx if need[0] else None, dw13 if need[1] else None, dw2 if need[2] else None
 
 
@@ -749,7 +765,14 @@ def bi_mx4_quantize(x, q=None, scales=None, stream=None):
     pq, ps, R2, K2 = _mx4_operand(q, scales, "q", dev)
     if R2 != R or K2 != K:
         raise ValueError("q must be [R, K/2]")
-    _launch("bi_mx4_quantize", dev, stream, px, f32, ldx, pq, ps, R, K)
+    if dev != _current_device():  # the call runs with the tensors' device current
+        with torch.cuda.device(dev):
+            return bi_mx4_quantize(x, q, scales, stream)
+    f = _fns.get("bi_mx4_quantize") or _bind("bi_mx4_quantize")
+    st = f(px, f32, ldx, pq, ps, R, K,
+           _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _fail("bi_mx4_quantize", st)
     return q, scales
 
 
@@ -761,7 +784,14 @@ def bi_mx4_dequantize(q, scales, out=None, dtype=torch.bfloat16, stream=None):
         out = torch.empty(R, K, dtype=dtype, device=q.device)
     f32 = out.dtype is _F32
     po, ldo = _rows(out, _F32 if f32 else _BF, "out", R, K, dev)
-    _launch("bi_mx4_dequantize", dev, stream, pq, ps, po, f32, ldo, R, K)
+    if dev != _current_device():  # the call runs with the tensors' device current
+        with torch.cuda.device(dev):
+            return bi_mx4_dequantize(q, scales, out, dtype, stream)
+    f = _fns.get("bi_mx4_dequantize") or _bind("bi_mx4_dequantize")
+    st = f(pq, ps, po, f32, ldo, R, K,
+           _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _fail("bi_mx4_dequantize", st)
     return out
 
 
@@ -776,7 +806,14 @@ def bi_mx4_gemm(xq, xs, wq, ws, addend=None, out=None, stream=None):
     if out is None:
         out = torch.empty(M, N, dtype=_BF, device=xq.device)
     po, ldo = _rows(out, _BF, "out", M, N, dev)
-    _launch("bi_mx4_gemm", dev, stream, px, pxs, pw, pws, pa, lda, po, ldo, M, N, K)
+    if dev != _current_device():  # the call runs with the tensors' device current
+        with torch.cuda.device(dev):
+            return bi_mx4_gemm(xq, xs, wq, ws, addend, out, stream)
+    f = _fns.get("bi_mx4_gemm") or _bind("bi_mx4_gemm")
+    st = f(px, pxs, pw, pws, pa, lda, po, ldo, M, N, K,
+           _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _fail("bi_mx4_gemm", st)
     return out
 
 
@@ -791,5 +828,12 @@ def bi_mx4_gate_up(xq, xs, w13q, w13s, out=None, stream=None):
     if out is None:
         out = torch.empty(M, N // 2, dtype=_BF, device=xq.device)
     po, ldo = _rows(out, _BF, "out", M, N // 2, dev)
-    _launch("bi_mx4_gate_up", dev, stream, px, pxs, pw, pws, po, ldo, M, N // 2, K)
+    if dev != _current_device():  # the call runs with the tensors' device current
+        with torch.cuda.device(dev):
+            return bi_mx4_gate_up(xq, xs, w13q, w13s, out, stream)
+    f = _fns.get("bi_mx4_gate_up") or _bind("bi_mx4_gate_up")
+    st = f(px, pxs, pw, pws, po, ldo, M, N // 2, K,
+           _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _fail("bi_mx4_gate_up", st)
     return out

@@ -578,8 +578,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
 // memory in slice order from +0 -- the recipe of the pair kernel, so the bits
 // are the same.  (Sending the partials instead, one 32-bit store each, took
 // 5 us for 32 rows x 48 tokens; reading them takes 0.7 us.)
-//   * A row tile is 128, 64 or 32 rows, so that there are about as many CTAs as
-//     SMs; up to 64 rows the MMA is an M=64 one (24 cycles each at N=16
+//   * A row tile is 128, 64 or 32 rows, so that there are more CTAs than SMs (two
+//     fit on one); up to 64 rows the MMA is an M=64 one (24 cycles each at N=16
 //     instead of 40).  Rows past the tile's read whatever shared memory holds,
 //     in accumulator rows that nothing reads.
 //   * A CTA keeps to half of an SM's shared memory, so that the down kernel's
@@ -990,11 +990,16 @@ static FfnGemm plan(int64_t rows, int64_t cols, int64_t K, int64_t slice, int ti
 // reduction has at most kPMaxSlices slices.
 static std::atomic<int> g_ffn_schedule{0};
 
+// Up to this many tokens the split kernel is the faster one (H=4096, I=2048: 128
+// tokens 24.8 us against 27.0, 192 tokens 41 against 28; H=2048, I=768: 12.5
+// against 13.7, 13.5 against 14.0).
+constexpr int64_t kSplitMaxM = 128;
+
 int set_ffn_schedule(int mode) { return g_ffn_schedule.exchange(mode); }
 
 static bool use_split(int64_t M, int64_t K) {
   const int mode = g_ffn_schedule.load();
-  return mode != 1 && (K + kSliceK - 1) / kSliceK <= kPMaxSlices && (mode == 2 || M <= kPMaxN);
+  return mode != 1 && (K + kSliceK - 1) / kSliceK <= kPMaxSlices && (mode == 2 || M <= kSplitMaxM);
 }
 
 // The split kernel over `rows` rows of A (gate/up: 2I interleaved ones) and M
@@ -1010,10 +1015,12 @@ static bi_status launch_split(FfnGemm g, int64_t rows, int64_t M, int64_t K, boo
   p.g = g;
   p.err = device_error_word();
   const int slices = div_up(K, kSliceK), token_tiles = div_up(M, g.n);
-  // the tallest tiles that still give four fifths of the SMs a CTA
+  // the tallest tiles that still give three CTAs to two SMs (H=4096, I=2048: 64
+  // rows a tile instead of 128 take 16.1 us instead of 18.7 for 32 tokens, 19.4
+  // instead of 22.9 for 64, the same for one)
   p.tile_rows = kFM;
   while (p.tile_rows > (A_MN ? 64 : 32) &&
-         static_cast<int64_t>(div_up(rows, p.tile_rows)) * slices * token_tiles * 5 < num_sms() * 4)
+         static_cast<int64_t>(div_up(rows, p.tile_rows)) * slices * token_tiles * 2 < num_sms() * 3)
     p.tile_rows /= 2;
   p.mma_rows = p.tile_rows > 64 ? 128 : 64;
   p.b_off = p.tile_rows * kPK * 2;
