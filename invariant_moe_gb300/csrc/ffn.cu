@@ -81,12 +81,13 @@ struct FfnMaps {
 };
 
 // The two projections' gradients from dact = d: one fixed fp32 sequence.
-__device__ __forceinline__ float gate_sigmoid(float g) { return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-g))); }
-__device__ __forceinline__ float dgate(float d, float g, float u) {
-  const float s = gate_sigmoid(g);
-  return __fmul_rn(__fmul_rn(__fmul_rn(d, u), s), __fmaf_rn(g, __fsub_rn(1.0f, s), 1.0f));
+struct GateGrads {
+  float dg, du;
+};
+__device__ __forceinline__ GateGrads gate_grads(float d, float g, float u) {
+  const float s = sigmoid_approx(g), ds = __fmul_rn(d, s);
+  return {__fmul_rn(__fmul_rn(ds, u), __fmaf_rn(g, __fsub_rn(1.0f, s), 1.0f)), __fmul_rn(ds, g)};
 }
-__device__ __forceinline__ float dup(float d, float g) { return __fmul_rn(__fmul_rn(d, g), gate_sigmoid(g)); }
 
 // 32 bytes to global memory: a whole sector per lane.
 __device__ __forceinline__ void store_32b(void *p, const uint32_t (&v)[8], bool wide) {
@@ -213,8 +214,9 @@ __device__ __forceinline__ void ffn_epilogue(const FfnGemm &p, const float (&acc
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const int h = j / 8, i = j % 8;
-        a[h][i] = __float_as_uint(dgate(acc[c][h][i], g[h][i], u[h][i]));
-        b[h][i] = __float_as_uint(dup(acc[c][h][i], g[h][i]));
+        const GateGrads r = gate_grads(acc[c][h][i], g[h][i], u[h][i]);
+        a[h][i] = __float_as_uint(r.dg);
+        b[h][i] = __float_as_uint(r.du);
       }
       const uint4 none[2] = {};
       store_rows32(stage, a, c * 16, dg, nullptr, none, lane);
@@ -639,8 +641,9 @@ __device__ __forceinline__ void ffn_store_one(const FfnGemm &p, int f, int t, fl
     static_cast<__nv_bfloat16 *>(p.out)[t * p.ldo + f] = __float2bfloat16_rn(d);
   } else {
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + static_cast<int64_t>(t) * 2 * p.rows + f;
-    o[0] = __float2bfloat16_rn(dgate(d, x.a, x.b));
-    o[p.rows] = __float2bfloat16_rn(dup(d, x.a));
+    const GateGrads r = gate_grads(d, x.a, x.b);
+    o[0] = __float2bfloat16_rn(r.dg);
+    o[p.rows] = __float2bfloat16_rn(r.du);
   }
 }
 

@@ -7,11 +7,21 @@
 
 namespace bimoe {
 
-// silu(g) * u: one fixed fp32 sequence (the fast exponential and divide are
-// within a few ulp of fp32, far below the bf16 rounding that follows; for g
-// below about -87 the denominator overflows and the quotient is the limit, 0).
+// 1 / (1 + exp(-g)) by the hardware's approximate exponential and reciprocal
+// (each within 2 ulp or so, far below the bf16 rounding that follows), with
+// subnormals flushed: as C++ intrinsics without flushing each takes several
+// instructions more, and the epilogues that need a sigmoid for every element
+// were bound by them.  For g below about -87 the result is 0, its limit.
+__device__ __forceinline__ float sigmoid_approx(float g) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(__fadd_rn(1.0f, e)));
+  return s;
+}
+
+// silu(g) * u: one fixed fp32 sequence.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  return __fmul_rn(__fdividef(g, __fadd_rn(1.0f, __expf(-g))), u);
+  return __fmul_rn(__fmul_rn(g, sigmoid_approx(g)), u);
 }
 
 // A row-major bf16 matrix [rows, cols] with row stride ld (elements).
