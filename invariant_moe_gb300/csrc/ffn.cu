@@ -154,7 +154,8 @@ __device__ __forceinline__ void ffn_epilogue(const FfnGemm &p, const float (&acc
     const RowsOut act{static_cast<__nv_bfloat16 *>(p.out) + static_cast<int64_t>(col0) * p.ldo + row0, p.ldo, limit,
                       p.rows - row0, true};
     const int64_t two = 2 * static_cast<int64_t>(p.rows);
-    float *gu = p.gu ? p.gu + col0 * two + row0 + (lane >> 2) : nullptr;
+    // the projections as 16-byte parts: part lane % 8 of a token's 16 gate and 16 up values
+    float *gu = p.gu ? p.gu + col0 * two + row0 + (lane & 3) * 4 + (lane & 4 ? p.rows : 0) : nullptr;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       if (c * 16 >= limit) break;
@@ -164,14 +165,26 @@ __device__ __forceinline__ void ffn_epilogue(const FfnGemm &p, const float (&acc
       store_rows16(stage, a, c * 16, act, lane);
       if (gu) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int t = c * 16 + (lane & 3) * 2 + (j & 1) + (j >> 2) * 8;
-          if (t < limit) {
-            float *o = gu + t * two + ((j >> 1) & 1) * 8;
-            __stcs(o, acc[c][0][j]);
-            __stcs(o + p.rows, acc[c][1][j]);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int t = (lane & 3) * 2 + (j & 1) + (j >> 2) * 8, f = h * 16 + (lane >> 2) + ((j >> 1) & 1) * 8;
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + static_cast<uint32_t>(t * kFPitch + f * 4)),
+                         "f"(acc[c][h][j])
+                         : "memory");
           }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = i * 4 + (lane >> 3);
+          float4 w;
+          asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                       : "=f"(w.x), "=f"(w.y), "=f"(w.z), "=f"(w.w)
+                       : "r"(stage + static_cast<uint32_t>(t * kFPitch + (lane & 7) * 16))
+                       : "memory");
+          if (c * 16 + t < limit) __stcs(reinterpret_cast<float4 *>(gu + (c * 16 + t) * two), w);
         }
+        __syncwarp();
       }
     }
   } else if constexpr (EPI == kStore) {
@@ -314,6 +327,13 @@ __global__ void __launch_bounds__(kFThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   griddep_wait();
+  // The dependent grid may start: its CTAs need an SM of their own (this one's
+  // shared memory is full), so they set up on SMs that are or become idle (a
+  // training step of 257 tokens, H=1040, I=720: 32.8 -> 29.2 us).  Not behind
+  // dact with wide tiles, whose long epilogue got slower by as much again with
+  // CTAs parked beside it (4096 tokens, H=2048, I=768: step 98 us, with it 104;
+  // with tiles of 32 columns, 257 tokens, 30.2 without and 29.2 with it).
+  if (EPI != kDact || one.n <= 64) griddep_launch_dependents();
 
   auto wait = [&](uint32_t bar, uint32_t parity, volatile int *ab) { return mbar_wait_cl(bar, parity, ab, batch.err); };
   // A tile: its problem, first row and column (of the pair), K steps and slices.

@@ -147,6 +147,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   griddep_wait();
+  // the dependent grid may start: its CTAs need an SM of their own
+  griddep_launch_dependents();
 
   auto wait = [&](uint32_t bar, uint32_t parity, volatile int *ab) {
     return PAIR ? mbar_wait_cl(bar, parity, ab, prm.err) : mbar_wait(bar, parity, ab, prm.err);
