@@ -320,3 +320,20 @@ def test_schedules_agree(cuda, M, H, I):
         bm.bi_ffn_schedule(old)
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(cuda):
+    """More than 2^31 saved projections: the last tokens' rows are those of a small call."""
+    import invariant_moe_gb300 as bm
+    M, H, I, n = (1 << 20) + 77, 16, 1040, 150
+    _, w13, w2, _, _ = (t.to(cuda) for t in make(1, H, I, 130))
+    x = syn.normal((M, H), 1.0, 131, BF, device="cuda")
+    dout = syn.normal((M, H), 1.0, 132, BF, device="cuda")
+    out, gu, act = bm.bi_ffn_forward_train(x, w13, w2)
+    assert gu.numel() > 1 << 31
+    dx = bm.bi_ffn_backward(dout, x, w13, w2, gu, act, need=(True, False, False))[0]
+    for s in (slice(M - n, M), slice((1 << 31) // (2 * I) - 5, (1 << 31) // (2 * I) + n)):
+        o, g, a = bm.bi_ffn_forward_train(x[s], w13, w2)
+        assert torch.equal(o, out[s]) and torch.equal(g, gu[s]) and torch.equal(a, act[s])
+        d = bm.bi_ffn_backward(dout[s], x[s], w13, w2, g, a, need=(True, False, False))[0]
+        assert torch.equal(d, dx[s])

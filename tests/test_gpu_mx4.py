@@ -250,3 +250,23 @@ def test_refusals(cuda):
     with pytest.raises(bm.BimoeError) as e:
         bm.bi_mx4_quantize(big[:, 4:68])
     assert e.value.status == 1
+
+
+def test_offsets_past_32_bits(cuda):
+    """More than 2^32 values: the last rows are those of a small call."""
+    import invariant_moe_gb300 as bm
+    R, K, N, n = (1 << 20) + 200, 4128, 2064, 130
+    x = syn.normal((R // 8, K), 1.0, 71, BF, device="cuda").repeat(8, 1)
+    x = torch.cat((x, syn.normal((R - x.shape[0], K), 1.0, 72, BF, device="cuda"))) if x.shape[0] < R else x
+    x[-n:] = syn.normal((n, K), 1.0, 73, BF).to(cuda)
+    assert x.numel() > 1 << 32
+    q, s = bm.bi_mx4_quantize(x)
+    q2, s2 = bm.bi_mx4_quantize(x[-n:])
+    assert torch.equal(q[-n:], q2)
+    y = bm.bi_mx4_dequantize(q, s, out=x)
+    assert torch.equal(y[-n:], bm.bi_mx4_dequantize(q2, s2))
+    del x, y
+    wq, ws = bm.bi_mx4_quantize(syn.normal((N, K), K ** -0.5, 74, BF).to(cuda))
+    z = bm.bi_mx4_gemm(q, s, wq, ws)
+    assert z.numel() > 1 << 31
+    assert torch.equal(z[-n:], bm.bi_mx4_gemm(q2, s2, wq, ws))
