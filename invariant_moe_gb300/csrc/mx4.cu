@@ -215,8 +215,8 @@ bi_status launch_mx4_quantize(const void *x, bool f32, int64_t ldx, uint8_t *q, 
   const int64_t ktiles = (K + 127) / 128;
   const dim3 block(kQWarps * 32);
   if (f32)
-    return launch_chained(mx4_quantize_kernel<float, RawF32>, quant_grid(R, K), block, 0, s, 1, static_cast<const float *>(x),
-                          ldx, q, scales, R, K, ktiles);
+    return launch_chained(mx4_quantize_kernel<float, RawF32>, quant_grid(R, K), block, 0, s, 1,
+                          static_cast<const float *>(x), ldx, q, scales, R, K, ktiles);
   return launch_chained(mx4_quantize_kernel<__nv_bfloat16, RawBf16>, quant_grid(R, K), block, 0, s, 1,
                         static_cast<const __nv_bfloat16 *>(x), ldx, q, scales, R, K, ktiles);
 }
