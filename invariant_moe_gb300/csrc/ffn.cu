@@ -1036,17 +1036,51 @@ static FfnGemm plan(int64_t rows, int64_t cols, int64_t K, int64_t slice, int ti
 // reduction has at most kPMaxSlices slices.
 static std::atomic<int> g_ffn_schedule{0};
 
-// Up to this many tokens the split kernel is the faster one (H=4096, I=2048: 128
-// tokens 24.8 us against 27.0, 192 tokens 41 against 28; H=2048, I=768: 12.5
-// against 13.7, 13.5 against 14.0).
-constexpr int64_t kSplitMaxM = 128;
-
 int set_ffn_schedule(int mode) { return g_ffn_schedule.exchange(mode); }
 
-static bool use_split(int64_t M, int64_t K) {
-  const int mode = g_ffn_schedule.load();
-  return mode != 1 && (K + kSliceK - 1) / kSliceK <= kPMaxSlices && (mode == 2 || M <= kSplitMaxM);
+static int slices_of(int64_t K) { return static_cast<int>(std::min<int64_t>((K + kSliceK - 1) / kSliceK, 1 << 20)); }
+
+// Whether a product of `rows` result rows, reduction K and M tokens goes to the
+// split kernel; `limit` is the number of tokens up to which it is the faster
+// one, by the reduction's slices (which it runs side by side, a pair one after
+// another) and by the product:
+//   gate/up and down  32 a slice of the longer reduction, as they go together
+//                     (forward, split and pairs in us: H=512, I=256 32 tokens
+//                     6.0, 7.6 and 64 8.4, 7.7; H=2048, I=768 64 tokens 10.4,
+//                     11.9 and 96 12.5, 12.0; H=4096, I=1024 128 tokens 16.9, 21.8)
+//   dact              32 up to two slices, then 32 a slice (with the weight
+//                     gradients: H=2048, I=768 32 tokens 12.8, 14.1 and 64 16.3,
+//                     14.8; H=2560, I=1024 96 tokens 20.9, 21.2; H=4096, I=2048
+//                     128 tokens 32.6, 37.4)
+//   dx                32 for each slice past the third: beside the weight
+//                     gradients, in their launch, it costs pairs little (what it
+//                     adds to the backward: H=4096, I=1024 one token 8.1, 5.2;
+//                     H=4096, I=2048 32 tokens 11.9, 15.1 and 64 14.3, 14.2)
+// and in one wave of two CTAs an SM, up to 32 tokens in two (forward, H=8192,
+// I=4096, two waves: one token 37.7, 46.0, 32 tokens 44.9, 48.2, 64 tokens 52.7,
+// 49.2; H=8192, I=2048, 80 tokens in two tiles, two waves: 44.7, 38.7; H=4096,
+// I=14336, three waves: one token 85.0, 83.0, 32 tokens 97.1, 86.2), for the
+// forward's two products together.
+constexpr int64_t kSplitMaxM = 128;
+
+static bool split_fits(int64_t M, int64_t rows, int64_t K) {
+  return slices_of(K) <= kPMaxSlices &&
+         (rows + kFM - 1) / kFM * slices_of(K) * ((M + kPMaxN - 1) / kPMaxN) <= (M <= 32 ? 4 : 2) * num_sms();
 }
+static bool use_split(int64_t M, int64_t rows, int64_t K, int64_t limit) {
+  const int mode = g_ffn_schedule.load();
+  if (mode == 2) return slices_of(K) <= kPMaxSlices;
+  return mode == 0 && M <= std::min(limit, kSplitMaxM) && split_fits(M, rows, K);
+}
+static int64_t forward_limit(int64_t M, int64_t H, int64_t I) {
+  return split_fits(M, 2 * I, H) && split_fits(M, H, I) ? 32 * std::max(slices_of(H), slices_of(I)) : 0;
+}
+static bool split_gate_up(int64_t M, int64_t H, int64_t I) { return use_split(M, 2 * I, H, forward_limit(M, H, I)); }
+static bool split_down(int64_t M, int64_t H, int64_t I) { return use_split(M, H, I, forward_limit(M, H, I)); }
+static bool split_dact(int64_t M, int64_t H, int64_t I) {
+  return use_split(M, I, H, slices_of(H) <= 2 ? 32 : 32 * slices_of(H));
+}
+static bool split_dx(int64_t M, int64_t H, int64_t I) { return use_split(M, H, 2 * I, 32 * (slices_of(2 * I) - 3)); }
 
 // The split kernel over `rows` rows of A (gate/up: 2I interleaved ones) and M
 // tokens.  map_a encodes A's tensor map for a given tile height.
@@ -1063,10 +1097,11 @@ static bi_status launch_split(FfnGemm g, int64_t rows, int64_t M, int64_t K, boo
   const int slices = div_up(K, kSliceK), token_tiles = div_up(M, g.n);
   // the tallest tiles that still give three CTAs to two SMs (H=4096, I=2048: 64
   // rows a tile instead of 128 take 16.1 us instead of 18.7 for 32 tokens, 19.4
-  // instead of 22.9 for 64, the same for one)
+  // instead of 22.9 for 64, the same for one), but not more than two to one
   p.tile_rows = kFM;
-  while (p.tile_rows > (A_MN ? 64 : 32) &&
-         static_cast<int64_t>(div_up(rows, p.tile_rows)) * slices * token_tiles * 2 < num_sms() * 3)
+  const auto ctas = [&](int tile) { return static_cast<int64_t>(div_up(rows, tile)) * slices * token_tiles; };
+  while (p.tile_rows > (A_MN ? 64 : 32) && ctas(p.tile_rows) * 2 < num_sms() * 3 &&
+         ctas(p.tile_rows / 2) <= num_sms() * 2)
     p.tile_rows /= 2;
   p.mma_rows = p.tile_rows > 64 ? 128 : 64;
   p.b_off = p.tile_rows * kPK * 2;
@@ -1110,7 +1145,7 @@ bi_status launch_ffn_gate_up(Mat x, const __nv_bfloat16 *w13, __nv_bfloat16 *act
   p.out = act;
   p.ldo = I;
   p.gu = gu;
-  if (use_split(M, H))
+  if (split_gate_up(M, H, I))
     return launch_split<kGateUp, false>(
         p, 2 * I, M, H, false,
         [&](CUtensorMap *a, int r) { return make_tma_inter_bf16(a, w13, I, I, H, r / 32); }, x.p, x.ld, s);
@@ -1127,7 +1162,7 @@ bi_status launch_ffn_down(const __nv_bfloat16 *act, const __nv_bfloat16 *w2, Mat
   p.ldo = ldo;
   p.addend = addend.p;
   p.ld_add = addend.ld;
-  if (use_split(M, I))  // launched behind launch_ffn_gate_up, which writes no weights: W2 may be read early
+  if (split_down(M, H, I))  // launched behind launch_ffn_gate_up, which writes no weights: W2 may be read early
     return launch_split<kStore, false>(
         p, H, M, I, true, [&](CUtensorMap *a, int r) { return make_tma_2d_bf16(a, w2, H, I, r); }, act, I, s);
   FfnMaps<1> m;
@@ -1141,7 +1176,7 @@ bi_status launch_ffn_dact(Mat dout, const __nv_bfloat16 *w2, const float *gu, __
   p.out = dgu;
   p.ldo = 2 * I;
   p.gu = const_cast<float *>(gu);
-  if (use_split(M, H))
+  if (split_dact(M, H, I))
     return launch_split<kDact, true>(
         p, I, M, H, false, [&](CUtensorMap *a, int) { return make_tma_2d_bf16(a, w2, H, I, kFK); }, dout.p, dout.ld, s);
   FfnMaps<1> m;
@@ -1193,7 +1228,7 @@ bi_status launch_ffn_grads(const FfnGrads &d, int64_t M, int64_t H, int64_t I, c
   dx.ldo = d.lddx;
   // One launch for all, or a launch each with 2 to 4 pairs a tile?  Decided as
   // if all three were asked for, so that a gradient's bits do not depend on that.
-  const bool dx_fits = use_split(M, 2 * I);  // dx by the split kernel
+  const bool dx_fits = split_dx(M, H, I);  // dx by the split kernel
   int n_w = 256, parts = 1;
   {
     int64_t best = INT64_MAX;
