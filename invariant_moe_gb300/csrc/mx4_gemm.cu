@@ -13,8 +13,8 @@
 //     token's row has the same bits in every batch.
 //   * Many tokens: CTA pairs (cta_group::2), 256 weight rows x up to 256 tokens,
 //     each CTA staging its own rows of W and half of the tokens.  Few: one CTA
-//     with 128, 64 or 32 weight rows (at their places in the 128-row scale tile)
-//     x up to 128 tokens, so that more CTAs stream the weights.
+//     with 128 weight rows x up to 128 tokens (tiles of 64 or 32 rows, so that
+//     more CTAs stream the weights, took the same time within 2 %).
 //   * Two accumulators of 256 columns and the scales do not fit the 512 columns
 //     of tensor memory: the second starts at column 224, and the epilogue drains
 //     the 32 shared columns first and then lets the next tile's MMAs go.
@@ -40,6 +40,7 @@ constexpr int kXRegsFew = 56, kXRegsMany = 224;  // 168 at launch: 128 x 56 + 25
 constexpr int kXRows = 128;          // weight rows per CTA
 constexpr int kXStageK = 256;        // values of k per stage
 constexpr int kXABytes = kXRows * kXStageK / 2;
+constexpr int scale_tiles(bool pair) { return pair ? 2 : 1; }  // scale tiles (128 tokens) that a token tile touches
 constexpr int kXMaxStages = 12;
 constexpr int kXAcc = 224;           // tensor-memory column of the second accumulator
 constexpr int kXSfA = 480;           // scales of A: 4 columns per 128 k
@@ -50,9 +51,7 @@ struct Mx4Gemm {
   int M, N;             // tokens, weight rows
   int nkb;              // stages of the reduction
   int n64;              // MMAs of the reduction
-  int rows;             // weight rows per tile (pair: 256)
   int n;                // tokens per tile (the MMA's N)
-  int sfb_tiles;        // scale tiles (128 tokens) that a token tile touches
   int m_tiles, n_tiles;
   int stages, stage_bytes;
   __nv_bfloat16 *y;
@@ -103,6 +102,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                     const __grid_constant__ Mx4Gemm prm) {
   constexpr int kCols = PAIR ? 128 : 64;  // columns of an epilogue warp
+  constexpr int kRows = PAIR ? 2 * kXRows : kXRows, kSfb = scale_tiles(PAIR);
   extern __shared__ uint8_t smem_raw[];
   uint8_t *aux = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
   auto wait = [&](uint32_t bar, uint32_t parity, volatile int *ab) {
     return PAIR ? mbar_wait_cl(bar, parity, ab, prm.err) : mbar_wait(bar, parity, ab, prm.err);
   };
-  auto row_of = [&](int tile) { return tile / prm.n_tiles * prm.rows + static_cast<int>(rank) * kXRows; };
+  auto row_of = [&](int tile) { return tile / prm.n_tiles * kRows + static_cast<int>(rank) * kXRows; };
   auto col_of = [&](int tile) { return tile % prm.n_tiles * prm.n; };
 
   if (warp < 4) {
@@ -172,9 +172,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
     if (warp == 0) {
       // -------------------------------------------------- TMA producer --
       if (elect_one()) {
-        const int a_rows = PAIR ? kXRows : prm.rows;
         const uint32_t bytes =
-            (PAIR ? 2u : 1u) * static_cast<uint32_t>((a_rows + b_rows) * 128 + (1 + prm.sfb_tiles) * 1024);
+            (PAIR ? 2u : 1u) * static_cast<uint32_t>((kXRows + b_rows) * 128 + (1 + kSfb) * 1024);
         uint32_t stage = 0, phase = 0, issued_mask = 0, issued_parity = 0;
         bool ok = true;
         for (int tile = unit0; tile < total && ok; tile += nunits) {
@@ -196,8 +195,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
             } else {
               const uint32_t fb = full0 + stage * 8;
               mbar_arrive_expect_tx(fb, bytes);
-              // the rows at their places in the 128-row scale tile
-              tma_load_2d(st + static_cast<uint32_t>(row % 128) * 128, &tmA, fb, kb * 128, row);
+              tma_load_2d(st, &tmA, fb, kb * 128, row);
               tma_load_2d(st + b_off, &tmB, fb, kb * 128, col);
               tma_load_2d(st + sfa_off, &tmSA, fb, kb * 256, row / 128);
               tma_load_2d(st + sfb_off, &tmSB, fb, kb * 256, col / 128);
@@ -228,8 +226,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     } else if (warp == 1) {
       // ---------------------------------------------------- MMA issuer --
       if (rank == 0 && elect_one()) {
-        const uint32_t m = PAIR ? 2 * kXRows : kXRows;
-        const uint32_t idesc0 = idesc_mxf4(m, prm.n, 0), idesc1 = idesc_mxf4(m, prm.n, 1);
+        const uint32_t idesc0 = idesc_mxf4(kRows, prm.n, 0), idesc1 = idesc_mxf4(kRows, prm.n, 1);
         const uint64_t a_first = sdesc_sw128(tiles0), b_first = sdesc_sw128(tiles0 + b_off);
         const uint64_t sa_first = sdesc_scales(tiles0 + sfa_off), sb_first = sdesc_scales(tiles0 + sfb_off);
         const uint32_t sfa = tmem_base + kXSfA, sfb0 = tmem_base + kXSfB;
@@ -257,11 +254,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
               if (PAIR) {
                 tmem_copy_scales_pair(sfa + 4 * c, sa_first + (at + c * 32));
                 tmem_copy_scales_pair(sfb0 + 8 * c, sb_first + (at + c * 32));
-                if (prm.sfb_tiles > 1) tmem_copy_scales_pair(sfb0 + 8 * c + 4, sb_first + (at + 64 + c * 32));
+                tmem_copy_scales_pair(sfb0 + 8 * c + 4, sb_first + (at + 64 + c * 32));
               } else {
                 tmem_copy_scales(sfa + 4 * c, sa_first + (at + c * 32));
                 tmem_copy_scales(sfb0 + 8 * c, sb_first + (at + c * 32));
-                if (prm.sfb_tiles > 1) tmem_copy_scales(sfb0 + 8 * c + 4, sb_first + (at + 64 + c * 32));
               }
             }
 #pragma unroll
@@ -311,9 +307,6 @@ __global__ void __launch_bounds__(kXThreads, 1)
     for (int tile = unit0; tile < total; tile += nunits) {
       if (!__all_sync(0xffffffffu, wait(tfull0 + buf * 8, buf_phase, abort_flag) ? 1 : 0)) break;
       tc_fence_after();
-      const int row = row_of(tile), place = PAIR ? 0 : row % 128;
-      // a tile of 32 or 64 rows sits at its place among the 128
-      const bool mine = PAIR || (q * 32 >= place && q * 32 < place + prm.rows);
       const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kXAcc +
                          static_cast<uint32_t>(h * ncols);
       uint32_t v[kCols / 16][2][8];
@@ -352,14 +345,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
         release();
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
-          if (mine && c * 16 < ncols) take(c);
+          if (c * 16 < ncols) take(c);
       }
       tmem_ld_wait();
       buf ^= 1u;
       if (buf == 0) buf_phase ^= 1u;
-      if (mine && ncols > 0)
-        mx4_epilogue<GATED, kChunks>(prm, v, (PAIR ? row : row / 128 * 128) + q * 32, col_of(tile) + h * ncols, ncols,
-                                     staging, lane);
+      if (ncols > 0)
+        mx4_epilogue<GATED, kChunks>(prm, v, row_of(tile) + q * 32, col_of(tile) + h * ncols, ncols, staging, lane);
     }
   }
 
@@ -442,41 +434,39 @@ bi_status launch_mx4_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *w
   p.addend = addend.p;
   p.ld_add = addend.ld;
   p.err = device_error_word();
-  // pairs when their largest tiles give at least half of them work
-  const int pairs = std::max(1, num_sms() / 2);
-  const bool pair = static_cast<int64_t>(div_up(N, 2 * kXRows)) * div_up(M, 256) * 2 >= pairs;
-  if (pair) {
-    // tokens per tile: 256, 192 or 128, the least waves x (columns + a tile's fixed cost)
-    p.rows = 2 * kXRows;
-    p.m_tiles = div_up(N, p.rows);
-    int64_t best = INT64_MAX;
-    for (int n = 256; n >= 128; n -= 64) {
-      const int64_t cost = (static_cast<int64_t>(p.m_tiles) * div_up(M, n) + pairs - 1) / pairs * (n + 32);
-      if (cost < best) {
-        best = cost;
-        p.n = n;
-      }
-    }
-    p.sfb_tiles = p.n > 128 ? 2 : 1;
-  } else {
-    // up to 128 tokens, rounded up to 16 (above 64: to 32, two halves of whole
-    // 16-column chunks), and the tallest tiles that still give every SM one
-    p.n = M > 64 ? std::min(128, div_up(M, 32) * 32) : div_up(M, 16) * 16;
-    p.sfb_tiles = 1;
-    p.rows = kXRows;
-    while (p.rows > 32 && static_cast<int64_t>(div_up(N, p.rows)) * div_up(M, p.n) < num_sms()) p.rows /= 2;
-    p.m_tiles = div_up(N, p.rows);
+  // One CTA or a pair, and the tokens per tile: the least time by fits (10 ns) to
+  // one to eight waves of N = 1024..32768, K = 1024..14336: a constant, and for
+  // each wave a constant and the stages.  In one wave the single CTAs win (us,
+  // single and pairs of 128: 4096 x 4096 gated, 256 tokens 6.5, 7.2; K = 14336,
+  // 512 tokens 16.1, 16.8; N = 14336, one token 6.6, 9.0), past it larger tiles do
+  // (8192 x 4096: 768 tokens 16.3 by single CTAs, 14.6 by pairs of 192; 1024
+  // tokens 20.1, 18.4 and, by pairs of 256, 16.7).
+  struct Form {
+    bool pair;
+    int n, once, wave, stage;
+  };
+  constexpr Form kForms[] = {{false, 128, 400, 100, 18}, {true, 192, 620, 70, 20}, {true, 256, 620, 60, 28}};
+  int64_t best = INT64_MAX;
+  bool pair = false;
+  for (const Form &f : kForms) {
+    const int64_t units = f.pair ? std::max(1, num_sms() / 2) : num_sms();
+    const int64_t tiles = static_cast<int64_t>(div_up(N, f.pair ? 2 * kXRows : kXRows)) * div_up(M, f.n);
+    const int64_t cost = f.once + (tiles + units - 1) / units * (f.wave + static_cast<int64_t>(f.stage) * p.nkb);
+    if (cost < best) best = cost, pair = f.pair, p.n = f.n;
   }
+  // few tokens rounded up to 16 (above 64 to 32, two halves of whole 16-column chunks)
+  if (!pair && M <= 128) p.n = M > 64 ? div_up(M, 32) * 32 : div_up(M, 16) * 16;
+  p.m_tiles = div_up(N, pair ? 2 * kXRows : kXRows);
   p.n_tiles = div_up(M, p.n);
   const int b_rows = pair ? p.n / 2 : p.n;
-  p.stage_bytes = kXABytes + div_up(b_rows * 128, 1024) * 1024 + 1024 + p.sfb_tiles * 1024;
+  p.stage_bytes = kXABytes + div_up(b_rows * 128, 1024) * 1024 + 1024 + scale_tiles(pair) * 1024;
   p.stages = std::min(kXMaxStages, (kXSmem - 2048 - 8 * kStageBytes) / p.stage_bytes);
   CUtensorMap maps[4];
   const int64_t ktiles = div_up(K, 128);
-  if (!make_tma_2d_u8(&maps[0], wq, N, K / 2, pair ? kXRows : p.rows) ||
+  if (!make_tma_2d_u8(&maps[0], wq, N, K / 2, kXRows) ||
       !make_tma_2d_u8(&maps[1], xq, M, K / 2, b_rows) ||
       !make_tma_mx_scales(&maps[2], ws, div_up(N, 128), ktiles, 1) ||
-      !make_tma_mx_scales(&maps[3], xs, div_up(M, 128), ktiles, p.sfb_tiles))
+      !make_tma_mx_scales(&maps[3], xs, div_up(M, 128), ktiles, scale_tiles(pair)))
     return BI_ERR_CUDA;
   if (pair) return gated ? launch_mx4<true, true>(maps, p, s) : launch_mx4<false, true>(maps, p, s);
   return gated ? launch_mx4<true, false>(maps, p, s) : launch_mx4<false, false>(maps, p, s);
