@@ -28,7 +28,7 @@
 // K = 8192 7.6 PFLOP/s.  Gated 4096 x 4096 x 4096: 25.7 us, 5.3 PFLOP/s.  One CTA
 // a tile of 192 tokens took 149 us for the first, a pair without the overlapping
 // accumulators' width (192 tokens) 89.6; blocks of 8 row tiles 84.9.  One token,
-// 4096 x 2048: 4.0 us, latency (4.5 MB are 0.7 us of copying).
+// 4096 x 2048: 3.8 us, latency (4.5 MB are 0.7 us of copying).
 #include <mutex>
 
 #include "tile_epilogue.cuh"
@@ -300,8 +300,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kXRegsMany));
     // -------------------------------------------------------- epilogue --
     const int q = warp & 3, h = (warp - 4) >> 2;
-    // columns of this warp: half of the tile's (a tile of up to 64: all for the first four warps)
-    const int ncols = prm.n > 64 ? prm.n / 2 : (h == 0 ? prm.n : 0);
+    // columns of this warp: half of the tile's (of 16 all for the first four warps)
+    const int ncols = prm.n > 16 ? prm.n / 2 : (h == 0 ? prm.n : 0);
     const uint32_t staging = tiles0 + static_cast<uint32_t>(prm.stages * prm.stage_bytes + (warp - 4) * kStageBytes);
     uint32_t buf = 0, buf_phase = 0;
     for (int tile = unit0; tile < total; tile += nunits) {
@@ -454,9 +454,16 @@ bi_status launch_mx4_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *w
     const int64_t cost = f.once + (tiles + units - 1) / units * (f.wave + static_cast<int64_t>(f.stage) * p.nkb);
     if (cost < best) best = cost, pair = f.pair, p.n = f.n;
   }
-  // few tokens rounded up to 16 (above 64 to 32, two halves of whole 16-column chunks)
-  if (!pair && M <= 128) p.n = M > 64 ? div_up(M, 32) * 32 : div_up(M, 16) * 16;
   p.m_tiles = div_up(N, pair ? 2 * kXRows : kXRows);
+  if (!pair) {
+    // In one wave 64 tokens a tile if that leaves it one: what follows the last copy
+    // is shorter (1001 x 2080, 100 tokens 6.7 us by a tile of 128, 5.4; 4096 x 2048,
+    // 256 tokens 5.2, 4.3).  (Not 32: a tile begins at the tensor-memory column of its tokens'
+    // scales, 32 tokens each, and an odd column is a misaligned address to the MMA.)
+    if (static_cast<int64_t>(p.m_tiles) * div_up(M, 64) <= num_sms()) p.n = 64;
+    // a single tile: no more than its tokens
+    if (M <= p.n) p.n = M <= 16 ? 16 : div_up(M, 32) * 32;
+  }
   p.n_tiles = div_up(M, p.n);
   const int b_rows = pair ? p.n / 2 : p.n;
   p.stage_bytes = kXABytes + div_up(b_rows * 128, 1024) * 1024 + 1024 + scale_tiles(pair) * 1024;

@@ -156,13 +156,14 @@ __device__ __forceinline__ void store_rows32(uint32_t stage, const uint32_t (&v)
                    : "memory");
       if (t < out.tokens && nf > 0) store_part(out.p + t * out.ld + f, w, nf);
     }
-  } else {  // a lane per feature, a token at a time
+  } else {  // a lane per feature, a token at a time (all read first: read and stored in turn took a latency each)
     uint16_t *q = reinterpret_cast<uint16_t *>(out.p) + static_cast<int64_t>(t0) * out.ld + lane;
+    uint16_t w[16];
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      const uint16_t w = lds16(stage + static_cast<uint32_t>(t * kStagePitch + lane * 2));
-      if (t0 + t < out.tokens && lane < out.feats) q[t * out.ld] = w;
-    }
+    for (int t = 0; t < 16; ++t) w[t] = lds16(stage + static_cast<uint32_t>(t * kStagePitch + lane * 2));
+#pragma unroll
+    for (int t = 0; t < 16; ++t)
+      if (t0 + t < out.tokens && lane < out.feats) q[t * out.ld] = w[t];
   }
   __syncwarp();
 }
@@ -188,11 +189,13 @@ __device__ __forceinline__ void store_rows16(uint32_t stage, const float (&v)[8]
   } else {  // a lane per feature, two tokens at a time
     const int f = lane & 15;
     uint16_t *q = reinterpret_cast<uint16_t *>(out.p) + static_cast<int64_t>(t0) * out.ld + f;
+    uint16_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = lds16(stage + static_cast<uint32_t>((2 * i + (lane >> 4)) * kPitch + f * 2));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int t = 2 * i + (lane >> 4);
-      const uint16_t w = lds16(stage + static_cast<uint32_t>(t * kPitch + f * 2));
-      if (t0 + t < out.tokens && f < out.feats) q[t * out.ld] = w;
+      if (t0 + t < out.tokens && f < out.feats) q[t * out.ld] = w[i];
     }
   }
   __syncwarp();
