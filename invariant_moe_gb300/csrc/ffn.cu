@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
 // Measured (weights not in L2): one token at H=4096, I=2048 14.8 us, of which the
 // 50 MB of weights take 7.4 at the copy bandwidth, two kernels' first copies 2,
 // their joins and stores 3, the boundary between them 1; 64 tokens 19.5 us.  At
-// H=2048, I=768: 8.2 us for one token, 10.3 for 33 (latency).
+// H=2048, I=768: 8.0 us for one token, 9.1 for 33 (latency).
 constexpr int kPThreads = 224;      // weight TMA, MMA, token TMA, 4 epilogue warps
 constexpr int kPMaxSlices = 8;      // CTAs of a cluster
 constexpr int kPK = 2 * kFK;        // reduction step of a stage

@@ -22,12 +22,12 @@
 //     registers before anything is stored.
 //
 // What bounds it, measured on a GB300.  An MMA of 128 rows x 256 columns x 64 k
-// takes 128 cycles a CTA: 9.7 PFLOP/s at 1.95 GHz.  8192 x 8192 x 4096: 82.6 us,
-// 6.7 PFLOP/s, a tile 9950 cycles of which 8190 are MMAs (the rest: handing the
+// takes 128 cycles a CTA: 9.7 PFLOP/s at 1.95 GHz.  8192 x 8192 x 4096: 79.6 us,
+// 6.9 PFLOP/s, a tile some 9900 cycles of which 8190 are MMAs (the rest: handing the
 // accumulator over, about 1400, and waits for copies), 14 waves for 13.5; with
-// K = 8192 7.6 PFLOP/s.  Gated 4096 x 4096 x 4096: 25.7 us, 5.3 PFLOP/s.  One CTA
+// K = 8192 7.6 PFLOP/s.  Gated 4096 x 4096 x 4096: 25.0 us, 5.5 PFLOP/s.  One CTA
 // a tile of 192 tokens took 149 us for the first, a pair without the overlapping
-// accumulators' width (192 tokens) 89.6; blocks of 8 row tiles 84.9.  One token,
+// accumulators' width (192 tokens) 89.6 (then 82.6 with it); blocks of 8 row tiles 84.9.  One token,
 // 4096 x 2048: 3.8 us, latency (4.5 MB are 0.7 us of copying).
 #include <mutex>
 
