@@ -22,7 +22,7 @@
 //     order, from +0, by the epilogue warps in registers while the next slice
 //     runs.  The recipe depends on the reduction length alone, so a token's row
 //     of out and dx has the same bits in every batch.  (The weight gradients
-//     reduce over the tokens: one slice, or as many as pairs share a tile.)
+//     reduce over the tokens, in one slice.)
 //   * Eight epilogue warps, 32 rows x half of the columns each, keep the tile in
 //     registers, so tensor memory is free again before anything is stored.
 //     gate/up: each CTA holds 64 gate rows and the matching 64 up rows in
@@ -67,8 +67,8 @@ constexpr int kFSmem = 1024 + kFStages * kFStageBytes + 256 + 8 * 16 * 144;  // 
 constexpr int kSliceK = 1024;                  // reduction slice of the recipe
 static_assert(kFSmem <= 227 * 1024, "shared memory");
 
-// kGrads: up to three problems in one launch, each kStore (dx) or kWgrad.
-enum FfnEpi { kGateUp, kStore, kDact, kWgrad, kGrads };
+// kGrads: up to three problems in one launch, each as kStore (dx) or a weight gradient.
+enum FfnEpi { kGateUp, kStore, kDact, kGrads };
 
 struct FfnGemm {
   int rows, cols;       // valid rows (A side; features) and columns (B side; tokens) of the result
@@ -80,9 +80,8 @@ struct FfnGemm {
   const __nv_bfloat16 *addend;  // kStore
   int64_t ld_add;
   float *gu;            // kGateUp: written (may be null); kDact: read
-  int mode;             // kWgrad: GradMode
-  int parts;            // kWgrad: CTA pairs of a cluster that share a tile's reduction
   int wgrad;            // kGrads: a weight gradient (B is MN-major too), else dx
+  int mode;             // a weight gradient's GradMode
 };
 
 // The problems of a launch and the tile numbers at which they begin.
@@ -285,11 +284,7 @@ __device__ __forceinline__ void ffn_wgrad_epilogue(const FfnGemm &p, const float
   }
 }
 
-// Columns that an epilogue warp finishes of a weight-gradient tile of n columns
-// shared by `parts` pairs: a multiple of 16, at most 64 for two pairs or more.
-__host__ __device__ constexpr int wgrad_share(int n, int parts) { return (n + 32 * parts - 1) / (32 * parts) * 16; }
-
-template <FfnEpi EPI, bool A_MN, bool B_MN>
+template <FfnEpi EPI, bool A_MN>
 __global__ void __launch_bounds__(kFThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ FfnMaps<EPI == kGrads ? 3 : 1> maps,
                     const __grid_constant__ FfnBatch<EPI == kGrads ? 3 : 1> batch) {
@@ -307,10 +302,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // rank in the pair; kWgrad: which of the cluster's pairs, and its K steps
-  const uint32_t crank = cluster_ctarank(), rank = crank & 1u, lead = crank & ~1u;
-  const int part = EPI == kWgrad ? static_cast<int>(crank >> 1) : 0;
-  const uint16_t pair_mask = static_cast<uint16_t>(3u << lead);
+  const uint32_t rank = cluster_ctarank();
   const int unit0 = static_cast<int>(cluster_id_x()), nunits = static_cast<int>(num_clusters_x());
   const int total = batch.first[kProblems];
 
@@ -353,10 +345,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
   if (EPI != kDact || one.n <= 64) griddep_launch_dependents();
 
   auto wait = [&](uint32_t bar, uint32_t parity, volatile int *ab) { return mbar_wait_cl(bar, parity, ab, batch.err); };
-  // A tile: its problem, first row and column (of the pair), K steps and slices.
+  // A tile: its problem, first row and column (of the pair).
   // Columns fastest: the tiles of a row block follow one another and share its A in L2.
   struct Tile {
-    int i, row, col, k_first, k_last, slice_kb;
+    int i, row, col;
   };
   auto tile_at = [&](int tile) {
     Tile t;
@@ -365,9 +357,6 @@ __global__ void __launch_bounds__(kFThreads, 1)
     const int local = tile - batch.first[t.i];
     t.row = local / g.n_tiles * (EPI == kGateUp ? kFM : 2 * kFM);
     t.col = local % g.n_tiles * g.n;
-    t.k_first = EPI == kWgrad ? g.nkb * part / g.parts : 0;
-    t.k_last = EPI == kWgrad ? g.nkb * (part + 1) / g.parts : g.nkb;
-    t.slice_kb = EPI == kWgrad ? t.k_last - t.k_first : g.slice_kb;
     return t;
   };
 
@@ -386,19 +375,19 @@ __global__ void __launch_bounds__(kFThreads, 1)
         for (int tile = unit0; tile < total && ok; tile += nunits) {
           const Tile ti = tile_at(tile);
           const CUtensorMap *tmA = &maps.a[ti.i], *tmB = &maps.b[ti.i];
-          const bool b_mn = EPI == kGrads ? batch.g[ti.i].wgrad != 0 : B_MN;
+          const bool b_mn = EPI == kGrads && batch.g[ti.i].wgrad != 0;
           const int half = batch.g[ti.i].n / 2;
           const uint32_t b_bytes =
               b_mn ? static_cast<uint32_t>((half + 63) / 64 * kFSlab) : static_cast<uint32_t>(half * kFK * 2);
           const int row = ti.row + static_cast<int>(rank) * (EPI == kGateUp ? kFM / 2 : kFM);
           const int col = ti.col + static_cast<int>(rank) * half;
-          for (int kb = ti.k_first; kb < ti.k_last; ++kb) {
+          for (int kb = 0; kb < batch.g[ti.i].nkb; ++kb) {
             if (!wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag)) {
               ok = false;
               break;
             }
             const uint32_t st = smem_u32(tiles + stage * kFStageBytes);
-            const uint32_t fb = mapa_shared(smem_u32(&full[stage]), lead);
+            const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
             if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[stage]), 2 * (kFABytes + b_bytes));
             const int k = kb * kFK;
             if (EPI == kGateUp) {
@@ -445,11 +434,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
         bool ok = true;
         for (int tile = unit0; tile < total && ok && !*abort_flag; tile += nunits) {
           const Tile ti = tile_at(tile);
-          const bool b_mn = EPI == kGrads ? batch.g[ti.i].wgrad != 0 : B_MN;
+          const bool b_mn = EPI == kGrads && batch.g[ti.i].wgrad != 0;
           const uint32_t idesc =
               idesc_bf16_f32(2 * kFM, batch.g[ti.i].n) | (A_MN ? kIdescAMn : 0u) | (b_mn ? kIdescBMn : 0u);
-          for (int kb0 = ti.k_first; kb0 < ti.k_last && ok; kb0 += ti.slice_kb) {
-            const int kb1 = min(ti.k_last, kb0 + ti.slice_kb);
+          const int nkb = batch.g[ti.i].nkb, slice_kb = batch.g[ti.i].slice_kb;
+          for (int kb0 = 0; kb0 < nkb && ok; kb0 += slice_kb) {
+            const int kb1 = min(nkb, kb0 + slice_kb);
             if (!wait(smem_u32(&tempty[buf]), buf_phase ^ 1u, abort_flag)) {
               ok = false;
               break;
@@ -469,14 +459,14 @@ __global__ void __launch_bounds__(kFThreads, 1)
                 const uint64_t bd = b_mn ? sdesc_sw128_mn(b0 + k * 2048, kFSlab) : sdesc_sw128(b0 + k * 32);
                 umma_f16_pair(d, ad, bd, idesc, (kb > kb0 || k) ? 1u : 0u);
               }
-              umma_commit_pair(smem_u32(&empty[stage]), pair_mask);
+              umma_commit_pair(smem_u32(&empty[stage]), 0x3);
               if (++stage == kFStages) {
                 stage = 0;
                 phase ^= 1u;
               }
             }
             if (!ok) break;
-            umma_commit_pair(smem_u32(&tfull[buf]), pair_mask);
+            umma_commit_pair(smem_u32(&tfull[buf]), 0x3);
             if (++buf == 2) {
               buf = 0;
               buf_phase ^= 1u;
@@ -484,13 +474,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
           }
         }
         // every MMA into both CTAs' tensor memory has completed
-        umma_commit_pair(smem_u32(drain), pair_mask);
+        umma_commit_pair(smem_u32(drain), 0x3);
         wait(smem_u32(drain), 0, nullptr);
       } else {
         return;
       }
     }
-    if (EPI == kWgrad && one.parts > 1) cluster_sync_rest();  // the partial tiles are there (see below)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFRegsMany));
     // -------------------------------------------------------- epilogue --
@@ -502,13 +491,13 @@ __global__ void __launch_bounds__(kFThreads, 1)
     for (int tile = unit0; tile < total && ok; tile += nunits) {
       const Tile ti = tile_at(tile);
       const FfnGemm &prm = batch.g[ti.i];
-      const bool wgrad = EPI == kGrads ? prm.wgrad != 0 : EPI == kWgrad;
+      const bool wgrad = EPI == kGrads && prm.wgrad != 0;
       const int ncols = prm.n / 2;  // columns of this warp: half h of the tile
       // the sums of the slices, in the order that the epilogue wants them
       float acc[8][2][8];
 #pragma unroll
       for (int c = 0; c < 128; ++c) acc[c / 16][c / 8 % 2][c % 8] = 0.0f;
-      for (int kb0 = ti.k_first; kb0 < ti.k_last; kb0 += ti.slice_kb) {
+      for (int kb0 = 0; kb0 < prm.nkb; kb0 += prm.slice_kb) {
         ok = __all_sync(0xffffffffu, wait(smem_u32(&tfull[buf]), buf_phase, abort_flag) ? 1 : 0) != 0;
         if (!ok) break;
         tc_fence_after();
@@ -536,7 +525,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[buf]), lead));
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&tempty[buf]), 0));
         if (++buf == 2) {
           buf = 0;
           buf_phase ^= 1u;
@@ -546,54 +535,15 @@ __global__ void __launch_bounds__(kFThreads, 1)
       const int row0 = ti.row + static_cast<int>(rank) * (EPI == kGateUp ? kFM / 2 : kFM) +
                        q * (EPI == kGateUp ? 16 : 32);
       const int col0 = ti.col + h * ncols;
-      if constexpr (EPI == kWgrad || EPI == kGrads) {
+      if constexpr (EPI == kGrads) {
         if (wgrad) {
           float flat[128];
 #pragma unroll
           for (int c = 0; c < 128; ++c) flat[c] = acc[c / 16][c / 8 % 2][c % 8];
-          if (EPI == kGrads || prm.parts == 1) {
-            ffn_wgrad_epilogue(prm, flat, row0, col0, ncols, lane);
-          } else {
-            // the partial tile [column][row], over the stages: all of this CTA's
-            // copies and MMAs are done
-            float *to = reinterpret_cast<float *>(tiles) + static_cast<size_t>(h * ncols) * kFM + q * 32 + lane;
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c < ncols) to[c * kFM] = flat[c];
-          }
+          ffn_wgrad_epilogue(prm, flat, row0, col0, ncols, lane);
         }
       }
-      if constexpr (EPI != kWgrad) {
-        if (!wgrad) ffn_epilogue<EPI == kGrads ? kStore : EPI>(prm, acc, row0, col0, ncols, staging, lane);
-      }
-    }
-    if constexpr (EPI == kWgrad) {
-      if (one.parts > 1) {
-        // one tile per cluster: the pairs' partial sums are added in pair order
-        // from +0, each CTA finishing its rows of 1 / parts of the columns
-        cluster_sync_rest();
-        const Tile ti = tile_at(unit0);
-        const int share = wgrad_share(one.n, one.parts);  // columns of this warp, at most
-        const int c0 = part * 2 * share + h * share, ncols = min(share, one.n - c0);
-        const uint32_t at = smem_u32(tiles) + static_cast<uint32_t>((c0 * kFM + q * 32 + lane) * 4);
-        float sum[64];
-#pragma unroll
-        for (int c = 0; c < 64; ++c) sum[c] = 0.0f;
-        for (int s = 0; s < one.parts && ok; ++s) {
-          const uint32_t from = mapa_shared(at, static_cast<uint32_t>(2 * s) + rank);
-#pragma unroll
-          for (int c = 0; c < 64; c += 16) {
-            if (c >= ncols) break;
-            float v[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = ld_cluster_f32(from + static_cast<uint32_t>((c + j) * kFM * 4));
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sum[c + j] = __fadd_rn(sum[c + j], v[j]);
-          }
-        }
-        if (ok && ncols > 0)
-          ffn_wgrad_epilogue(one, sum, ti.row + static_cast<int>(rank) * kFM + q * 32, ti.col + c0, ncols, lane);
-      }
+      if (!wgrad) ffn_epilogue<EPI == kGrads ? kStore : EPI>(prm, acc, row0, col0, ncols, staging, lane);
     }
   }
 
@@ -932,7 +882,7 @@ __global__ void __launch_bounds__(kPThreads)
 }
 
 // ------------------------------------------------------------------- host --
-template <FfnEpi EPI, bool A_MN, bool B_MN, int N>
+template <FfnEpi EPI, bool A_MN, int N>
 static bi_status launch_ffn(const FfnMaps<N> &maps, FfnBatch<N> p, cudaStream_t s) {
   static std::mutex mu;
   static int max_units[64] = {};  // CTA pairs resident at once, per device
@@ -943,7 +893,7 @@ static bi_status launch_ffn(const FfnMaps<N> &maps, FfnBatch<N> p, cudaStream_t 
     set_error("device ordinal %d out of range", dev);
     return BI_ERR_CUDA;
   }
-  auto kern = ffn_gemm_kernel<EPI, A_MN, B_MN>;
+  auto kern = ffn_gemm_kernel<EPI, A_MN>;
   {
     std::lock_guard<std::mutex> lk(mu);
     if (max_units[dev] == 0 || setup.pending(dev)) {
@@ -980,16 +930,9 @@ static bi_status launch_ffn(const FfnMaps<N> &maps, FfnBatch<N> p, cudaStream_t 
     }
     p.first[i + 1] = static_cast<int>(tiles);
   }
-  // a tile per cluster where its pairs share the reduction (any number of clusters may wait)
-  const int parts = EPI == kWgrad ? p.g[0].parts : 1;
-  const int units = static_cast<int>(parts > 1 ? tiles : std::min<int64_t>(max_units[dev], tiles));
-  return launch_chained(kern, dim3(2 * parts * units), dim3(kFThreads), kFSmem, s, 2 * parts, maps, p);
+  const int units = static_cast<int>(std::min<int64_t>(max_units[dev], tiles));
+  return launch_chained(kern, dim3(2 * units), dim3(kFThreads), kFSmem, s, 2, maps, p);
 }
-
-// In tile_cost's unit (2 cycles): a kernel boundary, and joining the partial sums
-// of pairs that share a weight-gradient tile; and the fewest K steps of such a pair.
-constexpr int64_t kLaunchCost = 2500, kJoinCost = 2500;
-constexpr int kWgradMinSteps = 8;
 
 static int div_up(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
@@ -1009,7 +952,6 @@ static FfnGemm problem(int64_t rows, int64_t cols, int64_t K, int64_t slice, int
   p.n_tiles = div_up(cols, n);
   p.nkb = div_up(K, kFK);
   p.slice_kb = std::max(1, static_cast<int>(slice / kFK));
-  p.parts = 1;
   return p;
 }
 
@@ -1152,7 +1094,7 @@ bi_status launch_ffn_gate_up(Mat x, const __nv_bfloat16 *w13, __nv_bfloat16 *act
   FfnMaps<1> m;
   if (!make_tma_inter_bf16(m.a, w13, I, I, H) || !make_tma_2d_bf16_ld(m.b, x.p, M, H, x.ld, p.n / 2))
     return BI_ERR_CUDA;
-  return launch_ffn<kGateUp, false, false>(m, FfnBatch<1>{{p}, {}, nullptr}, s);
+  return launch_ffn<kGateUp, false>(m, FfnBatch<1>{{p}, {}, nullptr}, s);
 }
 
 bi_status launch_ffn_down(const __nv_bfloat16 *act, const __nv_bfloat16 *w2, Mat addend, __nv_bfloat16 *out,
@@ -1167,7 +1109,7 @@ bi_status launch_ffn_down(const __nv_bfloat16 *act, const __nv_bfloat16 *w2, Mat
         p, H, M, I, true, [&](CUtensorMap *a, int r) { return make_tma_2d_bf16(a, w2, H, I, r); }, act, I, s);
   FfnMaps<1> m;
   if (!make_tma_2d_bf16(m.a, w2, H, I, kFM) || !make_tma_2d_bf16(m.b, act, M, I, p.n / 2)) return BI_ERR_CUDA;
-  return launch_ffn<kStore, false, false>(m, FfnBatch<1>{{p}, {}, nullptr}, s);
+  return launch_ffn<kStore, false>(m, FfnBatch<1>{{p}, {}, nullptr}, s);
 }
 
 bi_status launch_ffn_dact(Mat dout, const __nv_bfloat16 *w2, const float *gu, __nv_bfloat16 *dgu, int64_t M, int64_t H,
@@ -1182,7 +1124,7 @@ bi_status launch_ffn_dact(Mat dout, const __nv_bfloat16 *w2, const float *gu, __
   FfnMaps<1> m;
   if (!make_tma_2d_bf16(m.a, w2, H, I, kFK) || !make_tma_2d_bf16_ld(m.b, dout.p, M, H, dout.ld, p.n / 2))
     return BI_ERR_CUDA;
-  return launch_ffn<kDact, true, false>(m, FfnBatch<1>{{p}, {}, nullptr}, s);
+  return launch_ffn<kDact, true>(m, FfnBatch<1>{{p}, {}, nullptr}, s);
 }
 
 // dx alone, for few tokens (the split kernel).
@@ -1195,22 +1137,13 @@ static bi_status launch_dx_split(const FfnGrads &d, int64_t M, int64_t H, int64_
       2 * I, s);
 }
 
-// A weight gradient alone, its tokens shared by `parts` pairs.
-static bi_status launch_wgrad(FfnGemm p, int parts, Mat a, Mat b, int64_t M, int64_t rows, int64_t cols,
-                              cudaStream_t s) {
-  p.parts = parts;
-  FfnMaps<1> m;
-  if (!make_tma_2d_bf16_ld(m.a, a.p, M, rows, a.ld, kFK) || !make_tma_2d_bf16_ld(m.b, b.p, M, cols, b.ld, kFK))
-    return BI_ERR_CUDA;
-  return launch_ffn<kWgrad, true, true>(m, FfnBatch<1>{{p}, {}, nullptr}, s);
-}
-
 // The products that need no more than dgu: dW13, dW2 and dx, as asked for.  In
 // one launch, longest tiles first: their tiles fill the CTA pairs together
 // (4096 tokens, H=2048, I=768: 48 + 24 + 128 tiles on 76 pairs; the backward
-// pass 65 us, with a launch each 91 us).  Where the weight gradients have few
-// tiles but many tokens, each has a launch of its own in which clusters of pairs
-// share a tile.
+// pass 65 us, with a launch each 91 us). 
+// (Clusters of pairs sharing a weight-gradient tile's tokens, in a launch before dx,
+// were slower in all but the smallest: 8191 tokens, H=I=512 53.3 us by two pairs,
+// 53.9 in one launch; 4096 tokens 36.1, 32.3; 2048 tokens, H=512, I=256 22.5, 14.6.)
 bi_status launch_ffn_grads(const FfnGrads &d, int64_t M, int64_t H, int64_t I, cudaStream_t s) {
   const int64_t pairs = std::max(1, num_sms() / 2), all = (M + kFK - 1) / kFK * kFK;
   const int nkb = div_up(M, kFK);
@@ -1226,25 +1159,18 @@ bi_status launch_ffn_grads(const FfnGrads &d, int64_t M, int64_t H, int64_t I, c
   FfnGemm dx = plan(H, M, 2 * I, kSliceK, 2 * kFM, 32);
   dx.out = d.dx;
   dx.ldo = d.lddx;
-  // One launch for all, or a launch each with 2 to 4 pairs a tile?  Decided as
-  // if all three were asked for, so that a gradient's bits do not depend on that.
+  // The width of the weight gradients' tiles, as if all three were asked for, so
+  // that a gradient's bits do not depend on that.
   const bool dx_fits = split_dx(M, H, I);  // dx by the split kernel
-  int n_w = 256, parts = 1;
-  {
-    int64_t best = INT64_MAX;
-    for (int n = 256; n >= 128; n -= 128) {
-      const int64_t t13 = tiles_of(wgrad(2 * I, H, n, nullptr)), t2 = tiles_of(wgrad(H, I, n, nullptr));
-      const int64_t tdx = dx_fits ? 0 : tiles_of(dx), c_dx = tile_cost(dx.n, dx.nkb), c_w = tile_cost(n, nkb);
-      // together: the work over the pairs, and half of the longest tile of imbalance
-      int64_t cost = std::max((t13 + t2) * c_w + tdx * c_dx, (std::max(c_w, tdx ? c_dx : 0)) * pairs) / pairs +
-                     std::max(c_w, tdx ? c_dx : 0) / 2;
-      if (cost < best) best = cost, n_w = n, parts = 1;
-      const int64_t dx_alone = tdx ? (tdx + pairs - 1) / pairs * c_dx + kLaunchCost : 0;
-      for (int q = 2; q <= 4 && nkb / q >= kWgradMinSteps && std::max(t13, t2) * q <= pairs; ++q) {
-        cost = 2 * (tile_cost(n, div_up(nkb, q)) + kJoinCost) + kLaunchCost + dx_alone;
-        if (cost < best) best = cost, n_w = n, parts = q;
-      }
-    }
+  int n_w = 256;
+  int64_t best = INT64_MAX;
+  for (int n = 256; n >= 128; n -= 128) {
+    const int64_t t13 = tiles_of(wgrad(2 * I, H, n, nullptr)), t2 = tiles_of(wgrad(H, I, n, nullptr));
+    const int64_t tdx = dx_fits ? 0 : tiles_of(dx), c_dx = tile_cost(dx.n, dx.nkb), c_w = tile_cost(n, nkb);
+    // the work over the pairs, and half of the longest tile of imbalance
+    const int64_t longest = std::max(c_w, tdx ? c_dx : 0);
+    const int64_t cost = std::max((t13 + t2) * c_w + tdx * c_dx, longest * pairs) / pairs + longest / 2;
+    if (cost <= best) best = cost, n_w = n;
   }
   const bool dx_split = d.dx && dx_fits;
   if (dx_split) {
@@ -1252,12 +1178,6 @@ bi_status launch_ffn_grads(const FfnGrads &d, int64_t M, int64_t H, int64_t I, c
     if (st != BI_OK) return st;
   }
   const Mat dgu{d.dgu, 2 * I}, act{d.act, I};
-  if (parts > 1) {
-    bi_status st = BI_OK;
-    if (d.dw13) st = launch_wgrad(wgrad(2 * I, H, n_w, d.dw13), parts, dgu, d.x, M, 2 * I, H, s);
-    if (st == BI_OK && d.dw2) st = launch_wgrad(wgrad(H, I, n_w, d.dw2), parts, d.dout, act, M, H, I, s);
-    if (st != BI_OK) return st;
-  }
   FfnBatch<3> b{};
   FfnMaps<3> m;
   int n = 0;
@@ -1273,13 +1193,13 @@ bi_status launch_ffn_grads(const FfnGrads &d, int64_t M, int64_t H, int64_t I, c
   const bool dx_first = with_dx && tile_cost(dx.n, dx.nkb) > tile_cost(n_w, nkb);
   auto add_dx = [&] { add(dx, Mat{d.w13, H}, dgu, 2 * I, M, H, 2 * I, dx.n / 2); };
   if (dx_first) add_dx();
-  if (parts == 1 && d.dw13) add(wgrad(2 * I, H, n_w, d.dw13), dgu, d.x, M, M, 2 * I, H, kFK);
-  if (parts == 1 && d.dw2) add(wgrad(H, I, n_w, d.dw2), d.dout, act, M, M, H, I, kFK);
+  if (d.dw13) add(wgrad(2 * I, H, n_w, d.dw13), dgu, d.x, M, M, 2 * I, H, kFK);
+  if (d.dw2) add(wgrad(H, I, n_w, d.dw2), d.dout, act, M, M, H, I, kFK);
   if (with_dx && !dx_first) add_dx();
   if (!ok) return BI_ERR_CUDA;
   if (n == 0) return BI_OK;
   for (int i = n; i < 3; ++i) m.a[i] = m.a[0], m.b[i] = m.b[0];  // (no tile uses them)
-  return launch_ffn<kGrads, true, false>(m, b, s);
+  return launch_ffn<kGrads, true>(m, b, s);
 }
 
 }  // namespace bimoe
