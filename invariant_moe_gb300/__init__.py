@@ -150,6 +150,23 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on_stream(stream, f, *args):
+    """f(*args) with ``stream`` current, for calls that allocate: what they allocate then comes from that
+    stream's memory pool, which hands nothing to other work before the kernels launched here have run, and
+    holds nothing that work pending on another stream still uses.  What f allocated and returns is also kept,
+    once dropped, until the work that the caller has put on the current stream by then is done."""
+    here = torch.cuda.current_stream(stream.device)
+    if isinstance(args[0], torch.Tensor) and args[0].is_cuda and args[0].device != stream.device:
+        raise ValueError(f"stream is on {stream.device}, expected {args[0].device}")
+    with torch.cuda.stream(stream):
+        out = f(*args)
+    if here.cuda_stream != stream.cuda_stream:
+        for t in out if isinstance(out, tuple) else (out,):
+            if t is not None and not any(t is a for a in args):
+                t.record_stream(here)
+    return out
+
+
 def device_error() -> int:
     """Read and clear the device error word (synchronises the device)."""
     lib = load_library()
@@ -596,6 +613,8 @@ def ffn_saved(M, I, device):
 def bi_ffn_forward(x, w13, w2, addend=None, out=None, workspace=None, stream=None):
     """out [M,H] bf16 = (silu(x Wg^T) * (x Wu^T)) W2^T (+ addend), w13 [2I,H] = [Wg; Wu],
     w2 [H,I]; x, addend and out may be rows of wider tensors (row stride a multiple of 8)."""
+    if stream is not None and (out is None or workspace is None):
+        return _on_stream(stream, bi_ffn_forward, x, w13, w2, addend, out, workspace)
     M, H, I = _check_ffn_shapes(x, w13, w2)
     dev = _device_of(x, "x")
     px, ldx = _rows(x, _BF, "x", M, H, dev)
@@ -619,6 +638,8 @@ def bi_ffn_forward(x, w13, w2, addend=None, out=None, workspace=None, stream=Non
 
 def bi_ffn_forward_train(x, w13, w2, addend=None, out=None, gu=None, act=None, stream=None):
     """bi_ffn_forward that keeps what bi_ffn_backward reads.  Returns (out, gu fp32 [M,2I], act bf16 [M,I])."""
+    if stream is not None and (out is None or gu is None or act is None):
+        return _on_stream(stream, bi_ffn_forward_train, x, w13, w2, addend, out, gu, act)
     M, H, I = _check_ffn_shapes(x, w13, w2)
     dev = _device_of(x, "x")
     px, ldx = _rows(x, _BF, "x", M, H, dev)
@@ -649,6 +670,8 @@ def bi_ffn_backward(dout, x, w13, w2, gu, act, dx=None, dw13=None, dw2=None, nee
     """(dx, dw13, dw2) from dout [M,H]; None for each that ``need`` does not ask for.  dw13 and dw2
     are bf16 (the default) or both fp32; with ``accumulate`` the gradients are added to the fp32
     tensors given."""
+    if stream is not None and (workspace is None or any(n and t is None for n, t in zip(need, (dx, dw13, dw2)))):
+        return _on_stream(stream, bi_ffn_backward, dout, x, w13, w2, gu, act, dx, dw13, dw2, need, accumulate, workspace)
     M, H, I = _check_ffn_shapes(x, w13, w2)
     dev = _device_of(x, "x")
     px, ldx = _rows(x, _BF, "x", M, H, dev)
@@ -751,6 +774,8 @@ def _mx4_operand(q, s, name, device):
 
 def bi_mx4_quantize(x, q=None, scales=None, stream=None):
     """(codes, scale tiles) of x [R,K], bf16 or fp32, K a multiple of 32; x may be rows of a wider tensor."""
+    if stream is not None and (q is None or scales is None):
+        return _on_stream(stream, bi_mx4_quantize, x, q, scales)
     if x.dim() != 2:
         raise ValueError("x must be [R, K]")
     R, K = x.shape
@@ -778,6 +803,8 @@ def bi_mx4_quantize(x, q=None, scales=None, stream=None):
 
 def bi_mx4_dequantize(q, scales, out=None, dtype=torch.bfloat16, stream=None):
     """The values [R,K] (bf16 or fp32, both exact) that codes and scale tiles stand for."""
+    if stream is not None and out is None:
+        return _on_stream(stream, bi_mx4_dequantize, q, scales, out, dtype)
     dev = _device_of(q, "q codes")
     pq, ps, R, K = _mx4_operand(q, scales, "q", dev)
     if out is None:
@@ -797,6 +824,8 @@ def bi_mx4_dequantize(q, scales, out=None, dtype=torch.bfloat16, stream=None):
 
 def bi_mx4_gemm(xq, xs, wq, ws, addend=None, out=None, stream=None):
     """out [M,N] bf16 = X W^T (+ addend) of two quantised matrices X [M,K], W [N,K]."""
+    if stream is not None and out is None:
+        return _on_stream(stream, bi_mx4_gemm, xq, xs, wq, ws, addend, out)
     dev = _device_of(xq, "x codes")
     px, pxs, M, K = _mx4_operand(xq, xs, "x", dev)
     pw, pws, N, K2 = _mx4_operand(wq, ws, "w", dev)
@@ -820,6 +849,8 @@ def bi_mx4_gemm(xq, xs, wq, ws, addend=None, out=None, stream=None):
 def bi_mx4_gate_up(xq, xs, w13q, w13s, out=None, stream=None):
     """act [M,I] bf16 = silu(X Wg^T) * (X Wu^T), the weight's rows interleaved by mx4_interleave_gate_up
     before they were quantised."""
+    if stream is not None and out is None:
+        return _on_stream(stream, bi_mx4_gate_up, xq, xs, w13q, w13s, out)
     dev = _device_of(xq, "x codes")
     px, pxs, M, K = _mx4_operand(xq, xs, "x", dev)
     pw, pws, N, K2 = _mx4_operand(w13q, w13s, "w13", dev)

@@ -11,8 +11,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (bi_ffn_backward, bi_ffn_forward, bi_ffn_forward_train, bi_mx4_gate_up, bi_mx4_gemm, bi_mx4_quantize,
-               moe_layer, mx4_interleave_gate_up)
+from . import (_on_stream, bi_ffn_backward, bi_ffn_forward, bi_ffn_forward_train, bi_mx4_gate_up, bi_mx4_gemm,
+               bi_mx4_quantize, moe_layer, mx4_interleave_gate_up)
 
 
 class _GatedFfn(torch.autograd.Function):
@@ -42,8 +42,11 @@ def gated_ffn(x, w13, w2, addend=None):
 def moe_layer_with_shared_expert(x, w_router, w13, w2, top_k, shared_w13, shared_w2, bias=None, stream=None):
     """moe_layer plus a bf16 shared expert on the same tokens, summed in fp32 before the one rounding of the
     sum.  Returns (out, scores, ids, wts); a token's row of out has the same bits in every batch."""
-    out, scores, ids, wts = moe_layer(x, w_router, w13, w2, top_k, bias=bias, stream=stream)
-    bi_ffn_forward(x, shared_w13, shared_w2, addend=out, out=out, stream=stream)
+    if stream is not None:
+        return _on_stream(stream, moe_layer_with_shared_expert, x, w_router, w13, w2, top_k, shared_w13, shared_w2,
+                          bias)
+    out, scores, ids, wts = moe_layer(x, w_router, w13, w2, top_k, bias=bias)
+    bi_ffn_forward(x, shared_w13, shared_w2, addend=out, out=out)
     return out, scores, ids, wts
 
 
@@ -57,10 +60,12 @@ class Mx4SharedExpert:
         self.w2, self.s2 = bi_mx4_quantize(w2)
 
     def __call__(self, x, addend=None, stream=None):
-        xq, xs = bi_mx4_quantize(x, stream=stream)
-        act = bi_mx4_gate_up(xq, xs, self.w13, self.s13, stream=stream)
-        aq, as_ = bi_mx4_quantize(act, stream=stream)
-        return bi_mx4_gemm(aq, as_, self.w2, self.s2, addend=addend, stream=stream)
+        if stream is not None:
+            return _on_stream(stream, self.__call__, x, addend)
+        xq, xs = bi_mx4_quantize(x)
+        act = bi_mx4_gate_up(xq, xs, self.w13, self.s13)
+        aq, as_ = bi_mx4_quantize(act)
+        return bi_mx4_gemm(aq, as_, self.w2, self.s2, addend=addend)
 
 
 def main():
