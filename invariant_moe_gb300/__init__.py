@@ -179,6 +179,8 @@ def device_error() -> int:
 
 # ----------------------------------------------------------------- router --
 def bi_cast_bf16_to_f32(x, out=None, stream=None):
+    if stream is not None and out is None:
+        return _on_stream(stream, bi_cast_bf16_to_f32, x)
     out = out if out is not None else torch.empty(x.shape, dtype=torch.float32, device=x.device)
     _call("bi_cast_bf16_to_f32", _ptr(x, torch.bfloat16, "x"), _ptr(out, torch.float32, "out", x.device),
           x.numel(), _stream(stream))
@@ -188,6 +190,8 @@ def bi_cast_bf16_to_f32(x, out=None, stream=None):
 def bi_router_gemm(x, w, bias=None, out=None, schedule=0, stream=None):
     """y[M,N] = x[M,K] @ w[N,K]^T (+ bias), fp32, batch-invariant recipe.  x is
     fp32 or bf16 (bf16 values are read as their exact fp32 values)."""
+    if stream is not None and out is None:
+        return _on_stream(stream, bi_router_gemm, x, w, bias, None, schedule)
     M, K = x.shape
     N = w.shape[0]
     if w.shape[1] != K:
@@ -209,6 +213,8 @@ def bi_router_gemm(x, w, bias=None, out=None, schedule=0, stream=None):
 
 def bi_router_gemm_splitk_negctl(x, w, bias=None, out=None, stream=None):
     """Negative control (tests only): K split depends on M."""
+    if stream is not None and out is None:
+        return _on_stream(stream, bi_router_gemm_splitk_negctl, x, w, bias)
     M, K = x.shape
     N = w.shape[0]
     out = out if out is not None else torch.empty(M, N, dtype=torch.float32, device=x.device)
@@ -221,6 +227,8 @@ def bi_router_gemm_splitk_negctl(x, w, bias=None, out=None, stream=None):
 # ------------------------------------------------------------------ top-k --
 def bi_topk(scores, top_k, ids=None, wts=None, probs=None, want_probs=False, stream=None):
     """(ids int32 [M,k], wts fp32 [M,k], probs fp32 [M,E] or None)."""
+    if stream is not None and (ids is None or wts is None or (want_probs and probs is None)):
+        return _on_stream(stream, bi_topk, scores, top_k, ids, wts, probs, want_probs)
     M, E = scores.shape
     dev = scores.device
     ids = ids if ids is not None else torch.empty(M, top_k, dtype=torch.int32, device=dev)
@@ -247,6 +255,8 @@ def moe_workspace(M, H, E, top_k, I, device):
 
 def bi_moe_forward(x, ids, wts, w13, w2, out=None, workspace=None, stream=None):
     """out[M,H] bf16 = batch-invariant SwiGLU MoE of x [M,H] bf16."""
+    if stream is not None and (out is None or workspace is None):
+        return _on_stream(stream, bi_moe_forward, x, ids, wts, w13, w2, out, workspace)
     M, H, E, I, top_k = _check_moe_shapes(x, ids, wts, w13, w2, out)
     dev = x.device
     out = out if out is not None else torch.empty(M, H, dtype=torch.bfloat16, device=dev)
@@ -278,6 +288,8 @@ def bi_moe_forward_noalloc(x, ids, wts, w13, w2, out=None, stream=None):
     caller workspace (for callers that cannot allocate device memory; the
     output tensor, if not given, is still allocated here by torch).  The call
     runs with x's device current, whose scratch array the library uses."""
+    if stream is not None and out is None:
+        return _on_stream(stream, bi_moe_forward_noalloc, x, ids, wts, w13, w2)
     M, H, E, I, top_k = _check_moe_shapes(x, ids, wts, w13, w2, out)
     dev = x.device
     if not x.is_cuda:
@@ -294,6 +306,8 @@ def bi_moe_forward_noalloc(x, ids, wts, w13, w2, out=None, stream=None):
 
 
 def bi_moe_permute(ids, E, offsets=None, perm=None, workspace=None, stream=None):
+    if stream is not None and (offsets is None or perm is None or workspace is None):
+        return _on_stream(stream, bi_moe_permute, ids, E, offsets, perm, workspace)
     M, top_k = ids.shape
     dev = ids.device
     lib = load_library()
@@ -310,6 +324,8 @@ def bi_moe_permute(ids, E, offsets=None, perm=None, workspace=None, stream=None)
 
 def bi_moe_gather(x, offsets, perm, top_k, x_perm=None, stream=None):
     """x_perm [M*top_k, H] bf16: token rows in expert order."""
+    if stream is not None and x_perm is None:
+        return _on_stream(stream, bi_moe_gather, x, offsets, perm, top_k)
     M, H = x.shape
     E = offsets.numel() - 1
     dev = x.device
@@ -322,6 +338,8 @@ def bi_moe_gather(x, offsets, perm, top_k, x_perm=None, stream=None):
 
 def bi_moe_gate_up(x_perm, offsets, perm, wts, w13, top_k, act=None, stream=None):
     """act [M*top_k, I] bf16 from gathered rows x_perm [M*top_k, H]."""
+    if stream is not None and act is None:
+        return _on_stream(stream, bi_moe_gate_up, x_perm, offsets, perm, wts, w13, top_k)
     P, H = x_perm.shape
     M = P // top_k
     E, twoI, _ = w13.shape
@@ -338,6 +356,8 @@ def bi_moe_gate_up(x_perm, offsets, perm, wts, w13, top_k, act=None, stream=None
 def bi_moe_gate_up_tokens(x, offsets, perm, wts, w13, top_k, act=None, stream=None):
     """act [M*top_k, I] bf16, the gate/up GEMM gathering the token rows of
     x [M, H] itself (no gathered copy)."""
+    if stream is not None and act is None:
+        return _on_stream(stream, bi_moe_gate_up_tokens, x, offsets, perm, wts, w13, top_k)
     M, H = x.shape
     E, twoI, _ = w13.shape
     I = twoI // 2
@@ -369,6 +389,8 @@ def bi_moe_decode_fused(mode):
 
 
 def bi_moe_down(act, offsets, perm, w2, M, top_k, contrib=None, stream=None):
+    if stream is not None and contrib is None:
+        return _on_stream(stream, bi_moe_down, act, offsets, perm, w2, M, top_k)
     E, H, I = w2.shape
     dev = act.device
     contrib = contrib if contrib is not None else torch.empty(M * top_k, H, dtype=torch.float32, device=dev)
@@ -381,6 +403,8 @@ def bi_moe_down(act, offsets, perm, w2, M, top_k, contrib=None, stream=None):
 def bi_moe_gather_routing(ids, wts, offsets, perm, experts_per_rank, lid=None, pw=None, stream=None):
     """(lid int32 [M*top_k], pw fp32 [M*top_k]): for each permuted position,
     the expert's index on the rank that owns it and the routing probability."""
+    if stream is not None and (lid is None or pw is None):
+        return _on_stream(stream, bi_moe_gather_routing, ids, wts, offsets, perm, experts_per_rank, lid, pw)
     M, top_k = ids.shape
     E = offsets.numel() - 1
     dev = ids.device
@@ -396,6 +420,8 @@ def bi_moe_gather_routing(ids, wts, offsets, perm, experts_per_rank, lid=None, p
 
 def bi_moe_scatter_contrib(rows, offsets, perm, M, top_k, contrib=None, stream=None):
     """contrib [M*top_k, H] fp32 with contrib[perm[p]] = rows[p] for p < offsets[E]."""
+    if stream is not None and contrib is None:
+        return _on_stream(stream, bi_moe_scatter_contrib, rows, offsets, perm, M, top_k)
     H = rows.shape[-1]
     E = offsets.numel() - 1
     dev = rows.device
@@ -407,6 +433,8 @@ def bi_moe_scatter_contrib(rows, offsets, perm, M, top_k, contrib=None, stream=N
 
 
 def bi_moe_combine(contrib, M, top_k, out=None, stream=None):
+    if stream is not None and out is None:
+        return _on_stream(stream, bi_moe_combine, contrib, M, top_k)
     H = contrib.shape[-1]
     dev = contrib.device
     out = out if out is not None else torch.empty(M, H, dtype=torch.bfloat16, device=dev)
@@ -419,6 +447,8 @@ def bi_moe_combine_consume(contrib, M, top_k, out=None, stream=None):
     """bi_moe_combine for a caller that never reads ``contrib`` again: its
     lines are dropped from L2 once summed, and its contents are indeterminate
     afterwards."""
+    if stream is not None and out is None:
+        return _on_stream(stream, bi_moe_combine_consume, contrib, M, top_k)
     H = contrib.shape[-1]
     dev = contrib.device
     out = out if out is not None else torch.empty(M, H, dtype=torch.bfloat16, device=dev)
@@ -433,6 +463,8 @@ def bi_router_topk(x, w, top_k, bias=None, out=None, want_probs=False, schedule=
     programmatic dependent of the router grid; schedule 10 forces the
     one-kernel cluster path for up to 4 rows, 1..9 a router schedule).  Returns
     (scores [M,N] fp32, ids [M,top_k] int32, wts [M,top_k] fp32, probs or None)."""
+    if stream is not None and (out is None or ids is None or wts is None or want_probs):
+        return _on_stream(stream, bi_router_topk, x, w, top_k, bias, out, want_probs, schedule, None, ids, wts)
     M, K = x.shape
     N = w.shape[0]
     dev = x.device
@@ -458,6 +490,8 @@ def bi_topk_window(scores, k, row_start=None, row_end=None, num_cols=None, out=N
     """Windowed per-row top-k: int32 [n_rows, k] window-relative columns of
     the k best in-window scores, ascending, -1 tail.  scores is fp32
     [n_rows, ld] with unit column stride (row stride ld >= num_cols)."""
+    if stream is not None and out is None:
+        return _on_stream(stream, bi_topk_window, scores, k, row_start, row_end, num_cols)
     if scores.dim() != 2 or scores.stride(1) != 1:
         raise ValueError("scores must be 2-D with unit column stride")
     n_rows = scores.shape[0]
@@ -485,6 +519,8 @@ def bi_moe_gemm_variant(variant):
 
 def bi_fp32_fma_probe(blocks, iters, stream=None, out=None):
     """Run the FP32 FMA throughput probe; returns its output tensor."""
+    if stream is not None and out is None:
+        return _on_stream(stream, bi_fp32_fma_probe, blocks, iters)
     if out is None:
         out = torch.empty(blocks * 256, dtype=torch.float32, device="cuda")
     elif out.numel() < blocks * 256:
@@ -505,6 +541,9 @@ def bi_moe_layer(x, w_router, w13, w2, top_k, bias=None, out=None, scores=None, 
     """Whole hot path of one MoE layer in one library call: router (on the
     bf16 tokens, read as their exact fp32 values) -> top-k -> experts.
     Returns (out, scores, ids, wts)."""
+    if stream is not None and any(t is None for t in (out, scores, ids, wts, workspace)):
+        return _on_stream(stream, bi_moe_layer, x, w_router, w13, w2, top_k, bias, out, scores, ids, wts,
+                          workspace)
     M, H = x.shape
     E, H2 = w_router.shape
     if H2 != H:
@@ -671,7 +710,8 @@ def bi_ffn_backward(dout, x, w13, w2, gu, act, dx=None, dw13=None, dw2=None, nee
     are bf16 (the default) or both fp32; with ``accumulate`` the gradients are added to the fp32
     tensors given."""
     if stream is not None and (workspace is None or any(n and t is None for n, t in zip(need, (dx, dw13, dw2)))):
-        return _on_stream(stream, bi_ffn_backward, dout, x, w13, w2, gu, act, dx, dw13, dw2, need, accumulate, workspace)
+        return _on_stream(stream, bi_ffn_backward, dout, x, w13, w2, gu, act, dx, dw13, dw2, need, accumulate,
+                          workspace)
     M, H, I = _check_ffn_shapes(x, w13, w2)
     dev = _device_of(x, "x")
     px, ldx = _rows(x, _BF, "x", M, H, dev)

@@ -87,7 +87,8 @@ def tensors():
     z = torch.zeros
     return {"x": z(M, H, dtype=BF), "w13": z(2 * I, H, dtype=BF), "w2": z(H, I, dtype=BF),
             "gu": z(M, 2 * I), "act": z(M, I, dtype=BF), "q": z(M, K // 2, dtype=torch.uint8),
-            "s": z(1, 1, 512, dtype=torch.uint8), "wq": z(2 * I, K // 2, dtype=torch.uint8)}
+            "s": z(1, 1, 512, dtype=torch.uint8), "wq": z(2 * I, K // 2, dtype=torch.uint8),
+            **routed()}
 
 
 def expert():
@@ -99,6 +100,15 @@ def expert():
 
 
 E, TOPK = 4, 2
+
+
+def routed():
+    """Arguments of the routed experts' calls."""
+    z = torch.zeros
+    return {"scores": z(M, E), "w_router": z(E, H), "e13": z(E, 2 * I, H, dtype=BF), "e2": z(E, H, I, dtype=BF),
+            "ids": z(M, TOPK, dtype=torch.int32), "wts": z(M, TOPK), "off": z(E + 1, dtype=torch.int32),
+            "perm": z(M * TOPK, dtype=torch.int32), "xp": z(M * TOPK, H, dtype=BF),
+            "actp": z(M * TOPK, I, dtype=BF), "contrib": z(M * TOPK, H)}
 
 
 def layer(t, s):
@@ -118,6 +128,25 @@ CALLS = {
     "mx4_gate_up": lambda t, s: bm.bi_mx4_gate_up(t["q"], t["s"], t["wq"], t["s"], stream=s),
     "Mx4SharedExpert": lambda t, s: expert()(t["x"], stream=s),
     "moe_layer_with_shared_expert": layer,
+    # the routed experts' calls
+    "cast": lambda t, s: bm.bi_cast_bf16_to_f32(t["x"], stream=s),
+    "router_gemm": lambda t, s: bm.bi_router_gemm(t["x"], t["w_router"], stream=s),
+    "router_gemm_splitk_negctl": lambda t, s: bm.bi_router_gemm_splitk_negctl(t["x"], t["w_router"], stream=s),
+    "topk": lambda t, s: bm.bi_topk(t["scores"], TOPK, want_probs=True, stream=s),
+    "router_topk": lambda t, s: bm.bi_router_topk(t["x"], t["w_router"], TOPK, want_probs=True, stream=s),
+    "moe_forward": lambda t, s: bm.bi_moe_forward(t["x"], t["ids"], t["wts"], t["e13"], t["e2"], stream=s),
+    "moe_layer": lambda t, s: bm.moe_layer(t["x"], t["w_router"], t["e13"], t["e2"], TOPK, stream=s),
+    "permute": lambda t, s: bm.bi_moe_permute(t["ids"], E, stream=s),
+    "gather": lambda t, s: bm.bi_moe_gather(t["x"], t["off"], t["perm"], TOPK, stream=s),
+    "gate_up": lambda t, s: bm.bi_moe_gate_up(t["xp"], t["off"], t["perm"], t["wts"], t["e13"], TOPK, stream=s),
+    "gate_up_tokens": lambda t, s: bm.bi_moe_gate_up_tokens(t["x"], t["off"], t["perm"], t["wts"], t["e13"], TOPK,
+                                                            stream=s),
+    "down": lambda t, s: bm.bi_moe_down(t["actp"], t["off"], t["perm"], t["e2"], M, TOPK, stream=s),
+    "gather_routing": lambda t, s: bm.bi_moe_gather_routing(t["ids"], t["wts"], t["off"], t["perm"], E, stream=s),
+    "scatter_contrib": lambda t, s: bm.bi_moe_scatter_contrib(t["xp"], t["off"], t["perm"], M, TOPK, stream=s),
+    "combine": lambda t, s: bm.bi_moe_combine(t["contrib"], M, TOPK, stream=s),
+    "combine_consume": lambda t, s: bm.bi_moe_combine_consume(t["contrib"], M, TOPK, stream=s),
+    "fp32_fma_probe": lambda t, s: bm.bi_fp32_fma_probe(1, 1, stream=s),
 }
 
 
@@ -131,7 +160,7 @@ def test_allocates_and_launches_on_the_stream_given(world, name):
     # what the call hands out may be used, and dropped, on the stream that was current
     given = {id(v) for v in t.values()}
     for r in out if isinstance(out, tuple) else (out,):
-        if id(r) not in given:
+        if r is not None and id(r) not in given:
             assert (id(r), world.here.cuda_stream) in world.recorded
 
 
