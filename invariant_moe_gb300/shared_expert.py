@@ -15,9 +15,20 @@ from . import (_on_stream, bi_ffn_backward, bi_ffn_forward, bi_ffn_forward_train
                bi_mx4_quantize, moe_layer, mx4_interleave_gate_up)
 
 
+def _rows16(t):
+    """t [M, cols], or a copy of it where its rows do not lie as the library takes them: unit column stride, a
+    row stride of at least cols and a multiple of 8, 16-byte aligned.  (Autograd hands out rows of stride 0
+    for a sum over the tokens, and slices at any column for a concatenation.)"""
+    rows, cols = t.shape
+    if t.stride(1) == 1 and (rows <= 1 or (t.stride(0) >= cols and t.stride(0) % 8 == 0)) and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w13, w2, addend):
+        x, addend = _rows16(x), None if addend is None else _rows16(addend)
         out, gu, act = bi_ffn_forward_train(x, w13, w2, addend=addend)
         ctx.save_for_backward(x, w13, w2, gu, act)
         return out
@@ -25,8 +36,7 @@ class _GatedFfn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         x, w13, w2, gu, act = ctx.saved_tensors
-        if dout.stride(-1) != 1 or dout.stride(0) % 8:
-            dout = dout.contiguous()  # e.g. the expanded gradient of a sum
+        dout = _rows16(dout)
         dx, dw13, dw2 = bi_ffn_backward(dout, x, w13, w2, gu, act, need=ctx.needs_input_grad[:3])
         return dx, dw13, dw2, dout if ctx.needs_input_grad[3] else None
 
@@ -35,7 +45,7 @@ def gated_ffn(x, w13, w2, addend=None):
     """(silu(x Wg^T) * (x Wu^T)) W2^T (+ addend), differentiable in every argument; x [M,H], w13 [2I,H],
     w2 [H,I] and addend [M,H] bf16."""
     if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, w13, w2, addend))):
-        return bi_ffn_forward(x, w13, w2, addend=addend)
+        return bi_ffn_forward(_rows16(x), w13, w2, addend=None if addend is None else _rows16(addend))
     return _GatedFfn.apply(x, w13, w2, addend)
 
 

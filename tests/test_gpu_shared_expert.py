@@ -91,3 +91,28 @@ def test_example_runs(cuda, capsys):
     losses = [float(line.split()[-1]) for line in text.splitlines() if line.startswith("step")]
     assert losses[-1] < 0.2 * losses[0]
     assert "bit for bit: True" in text
+
+
+@pytest.mark.parametrize("how", ["sum_rows", "cat", "transposed"])
+def test_gradients_of_any_layout(cuda, how):
+    """Expanded, misaligned and transposed gradients give the bits of the same gradient laid out plainly."""
+    from invariant_moe_gb300.shared_expert import gated_ffn
+    M, H, I = 45, 160, 96
+    v = syn.normal((H,), 1.0, 41, BF).to(cuda)
+
+    def reduce(o):
+        if how == "sum_rows":
+            return (o.sum(0) * v).sum()
+        if how == "cat":
+            z = torch.zeros(M, 4, dtype=BF, device=cuda)
+            return (torch.cat((z, o, z), 1) * torch.cat((v[:4], v, v[:4]))).sum()
+        return (o.t().contiguous() * v[:, None]).sum()
+
+    leaves = [t.requires_grad_() for t in make(M, H, I, 31, cuda)]
+    reduce(gated_ffn(*leaves)).backward()
+    got = [t.grad.clone() for t in leaves]
+    for t in leaves:
+        t.grad = None
+    gated_ffn(*leaves).backward(v.expand(M, H).contiguous())
+    for a, t in zip(got, leaves):
+        assert torch.equal(a, t.grad)
