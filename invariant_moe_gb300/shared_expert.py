@@ -25,6 +25,24 @@ def _rows16(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
+def _gradients(need, dout, x, w13, w2, gu, act):
+    return bi_ffn_backward(dout, x, w13, w2, gu, act, need=need)
+
+
+class _FfnGradients(torch.autograd.Function):
+    """The backward pass as a node of its own: where a gradient is taken with create_graph=True its results stay
+    connected to what they depend on, so that a second derivative, which the library does not have, is refused
+    instead of counted as zero."""
+
+    @staticmethod
+    def forward(ctx, *args):
+        return _gradients(*args)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("gated_ffn has no second derivative (it came up in a gradient of its gradients)")
+
+
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w13, w2, addend):
@@ -37,12 +55,13 @@ class _GatedFfn(torch.autograd.Function):
     def backward(ctx, dout):
         x, w13, w2, gu, act = ctx.saved_tensors
         dout = _rows16(dout)
-        dx, dw13, dw2 = bi_ffn_backward(dout, x, w13, w2, gu, act, need=ctx.needs_input_grad[:3])
+        gradients = _FfnGradients.apply if torch.is_grad_enabled() else _gradients
+        dx, dw13, dw2 = gradients(ctx.needs_input_grad[:3], dout, x, w13, w2, gu, act)
         return dx, dw13, dw2, dout if ctx.needs_input_grad[3] else None
 
 
 def gated_ffn(x, w13, w2, addend=None):
-    """(silu(x Wg^T) * (x Wu^T)) W2^T (+ addend), differentiable in every argument; x [M,H], w13 [2I,H],
+    """(silu(x Wg^T) * (x Wu^T)) W2^T (+ addend), differentiable once in every argument; x [M,H], w13 [2I,H],
     w2 [H,I] and addend [M,H] bf16."""
     if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, w13, w2, addend))):
         return bi_ffn_forward(_rows16(x), w13, w2, addend=None if addend is None else _rows16(addend))

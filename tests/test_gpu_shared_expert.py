@@ -116,3 +116,16 @@ def test_gradients_of_any_layout(cuda, how):
     gated_ffn(*leaves).backward(v.expand(M, H).contiguous())
     for a, t in zip(got, leaves):
         assert torch.equal(a, t.grad)
+
+
+def test_second_order_is_refused(cuda):
+    """A gradient penalty raises; the first-order gradients of a graph that was asked for have their bits."""
+    from invariant_moe_gb300.shared_expert import gated_ffn
+    leaves = [t.requires_grad_() for t in make(37, 144, 112, 51, cuda)]
+    out = gated_ffn(*leaves)
+    grads = torch.autograd.grad(out.sum(), leaves, create_graph=True)
+    want = torch.autograd.grad(gated_ffn(*leaves).sum(), leaves)
+    for t, g, w in zip(leaves, grads, want):
+        assert torch.equal(g, w) and g.requires_grad
+        with pytest.raises(RuntimeError, match="second"):
+            torch.autograd.grad(g.float().square().sum(), t, retain_graph=True)

@@ -94,3 +94,32 @@ def test_every_layout_of_the_tokens(formulas, grad):
     v = inside(16, 8)(x)
     assert se._rows16(v) is v
     assert se._rows16(x) is x
+
+
+def test_second_order_is_refused_where_it_is_needed(formulas):
+    """A gradient taken with create_graph=True keeps its place in the graph: what would need a second derivative
+    of the block raises, instead of losing that term; what does not need one has its value."""
+    x, w13, w2, add = [aligned(t).requires_grad_() for t in make(2)]
+    loss = se.gated_ffn(x, w13, w2, add).float().square().sum()
+    grads = torch.autograd.grad(loss, (x, w13, w2), create_graph=True)
+    for t, g in zip((x, w13, w2), grads):
+        assert g.requires_grad
+        with pytest.raises(RuntimeError, match="second"):
+            torch.autograd.grad(loss + g.float().square().sum(), t, retain_graph=True)
+    # a sum's gradient is a constant, dx depends on x all the same
+    out = se.gated_ffn(x, w13, w2)
+    g, = torch.autograd.grad(out.sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="second"):
+        (out.sum() + g.float().square().sum()).backward()
+    # first-order terms of a graph that was asked for are right
+    for t in (x, w13, w2, add):
+        t.grad = None
+    se.gated_ffn(x, w13, w2, add).sum().backward(create_graph=True)
+    r = ref.ffn(x.detach(), w13.detach(), w2.detach(), dout=torch.ones(M, H))
+    for t, n in ((x, "dx"), (w13, "dw13"), (w2, "dw2")):
+        assert torch.equal(t.grad.detach(), r[n].to(BF))
+    # the addend's gradient is dout itself, differentiable as that is
+    v = torch.randn(M, H).to(BF).requires_grad_()
+    g, = torch.autograd.grad((se.gated_ffn(x, w13, w2, add) * v).sum(), add, create_graph=True)
+    g2, = torch.autograd.grad(g.float().square().sum(), v)
+    assert torch.equal(g2, (2 * v.detach().float()).to(BF))
