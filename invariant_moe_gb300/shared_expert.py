@@ -10,6 +10,7 @@ bookkeeping runs in the library's kernels."""
 from __future__ import annotations
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import (_on_stream, bi_ffn_backward, bi_ffn_forward, bi_ffn_forward_train, bi_mx4_gate_up, bi_mx4_gemm,
                bi_mx4_quantize, moe_layer, mx4_interleave_gate_up)
@@ -61,9 +62,12 @@ class _GatedFfn(torch.autograd.Function):
 
 
 def gated_ffn(x, w13, w2, addend=None):
-    """(silu(x Wg^T) * (x Wu^T)) W2^T (+ addend), differentiable once in every argument; x [M,H], w13 [2I,H],
-    w2 [H,I] and addend [M,H] bf16."""
-    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, w13, w2, addend))):
+    """(silu(x Wg^T) * (x Wu^T)) W2^T (+ addend), differentiable once, in reverse mode, in every argument;
+    x [M,H], w13 [2I,H], w2 [H,I] and addend [M,H] bf16."""
+    args = [t for t in (x, w13, w2, addend) if t is not None]
+    # a tangent of forward-mode differentiation goes to the autograd function too, which refuses it
+    if not (torch.is_grad_enabled() and any(t.requires_grad for t in args)) and all(
+            unpack_dual(t).tangent is None for t in args):
         return bi_ffn_forward(_rows16(x), w13, w2, addend=None if addend is None else _rows16(addend))
     return _GatedFfn.apply(x, w13, w2, addend)
 

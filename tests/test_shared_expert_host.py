@@ -123,3 +123,20 @@ def test_second_order_is_refused_where_it_is_needed(formulas):
     g, = torch.autograd.grad((se.gated_ffn(x, w13, w2, add) * v).sum(), add, create_graph=True)
     g2, = torch.autograd.grad(g.float().square().sum(), v)
     assert torch.equal(g2, (2 * v.detach().float()).to(BF))
+
+
+@pytest.mark.parametrize("which", range(4))
+@pytest.mark.parametrize("no_grad", [False, True])
+def test_forward_mode_is_refused(formulas, which, no_grad):
+    """A tangent on any argument raises; without one the call is as ever inside a dual level."""
+    from torch.autograd import forward_ad
+    args = [aligned(t) for t in make(3)]
+    want = se.gated_ffn(*args)
+    with torch.set_grad_enabled(not no_grad), forward_ad.dual_level():
+        assert torch.equal(se.gated_ffn(*args), want)
+        dual = list(args)
+        dual[which] = forward_ad.make_dual(args[which], torch.ones_like(args[which]))
+        with pytest.raises((RuntimeError, NotImplementedError), match="forward"):
+            se.gated_ffn(*dual)
+    with torch.no_grad():
+        assert torch.equal(se.gated_ffn(*args), want)
