@@ -524,7 +524,9 @@ BI_API bi_status bi_ffn_forward_train(const bi_bf16 *x, int64_t ldx, const bi_bf
 /*
  * bi_ffn_backward -- gradients from dout [M,H] bf16 (row stride lddo).
  *   x, w13, w2: the forward's;  gu, act: kept by bi_ffn_forward_train
- *   dx   [M,H] bf16, row stride lddx, written, or NULL (not computed)
+ *   dx   [M,H] bf16, row stride lddx, written, or NULL (not computed); it must
+ *     not overlap dout where dw2 is computed, nor x where dw13 is
+ *     (BI_ERR_INVALID_ARG): those products read them while dx is stored
  *   dw13 [2I,H], dw2 [H,I], or NULL each (not computed)
  *   grad_mode: 0 dw13 and dw2 are bf16, written; 1 fp32, written; 2 fp32,
  *     the gradient is added to what they hold (micro-batches)

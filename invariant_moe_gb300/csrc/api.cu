@@ -6,6 +6,7 @@
 #include <cstdio>
 #include <atomic>
 #include <mutex>
+#include <utility>
 
 #include "bimoe_internal.cuh"
 #include "ffn_internal.cuh"
@@ -819,6 +820,21 @@ static bi_status check_rows(const char *name, const void *p, int64_t ld, int64_t
   return BI_OK;
 }
 
+// Whether matrices of `rows` x `cols` bf16 with row strides ldp and ldq share memory
+// (with different strides: whether their ranges do).
+static bool overlap(const void *p, int64_t ldp, const void *q, int64_t ldq, int64_t rows, int64_t cols) {
+  uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  if (a > b) {
+    std::swap(a, b);
+    std::swap(ldp, ldq);
+  }
+  const uintptr_t apart = (b - a) / sizeof(bi_bf16);  // b's first element, counted from a's
+  if (apart >= static_cast<uintptr_t>((rows - 1) * ldp + cols)) return false;
+  if (ldp != ldq) return true;
+  const int64_t at = static_cast<int64_t>(apart % static_cast<uintptr_t>(ldp));
+  return at < cols || at > ldp - cols;
+}
+
 static Mat mat(const bi_bf16 *p, int64_t ld) { return Mat{reinterpret_cast<const __nv_bfloat16 *>(p), ld}; }
 static const __nv_bfloat16 *cbf(const void *p) { return static_cast<const __nv_bfloat16 *>(p); }
 static __nv_bfloat16 *mbf(void *p) { return static_cast<__nv_bfloat16 *>(p); }
@@ -901,6 +917,9 @@ BI_API bi_status bi_ffn_backward(const bi_bf16 *dout, int64_t lddo, const bi_bf1
     const size_t need = static_cast<size_t>(M) * 2 * I * sizeof(bi_bf16);
     BI_REQUIRE(workspace && aligned(workspace, 256), BI_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     BI_REQUIRE(workspace_bytes >= need, BI_ERR_WORKSPACE, "workspace %zu < %zu bytes", workspace_bytes, need);
+    // dx is written beside the products that read dout (dW2) and x (dW13)
+    BI_REQUIRE(!(dx && dw2 && overlap(dx, lddx, dout, lddo, M, H)), BI_ERR_INVALID_ARG, "dx and dout overlap");
+    BI_REQUIRE(!(dx && dw13 && overlap(dx, lddx, x, ldx, M, H)), BI_ERR_INVALID_ARG, "dx and x overlap");
     BI_TRY(launch_ffn_dact(mat(dout, lddo), cbf(w2), gu, dgu, M, H, I, s));
   }
   const FfnGrads d{mat(dout, lddo), mat(x, ldx), dgu, cbf(act), cbf(w13), mbf(dx), lddx, dw13, dw2, grad_mode};
