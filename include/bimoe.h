@@ -730,6 +730,16 @@ BI_API bi_status bi_moe_decode_fused(int32_t mode, int32_t *previous);
 BI_API bi_status bi_ffn_schedule(int32_t mode, int32_t *previous);
 
 /*
+ * bi_mx4_form -- which form of the kernel runs bi_mx4_gemm and bi_mx4_gate_up,
+ * for the whole process from the next call on: 0 automatic (the default: by
+ * estimated time), 1 single CTAs of 128 weight rows, 2 CTA pairs with 192
+ * tokens a tile, 3 CTA pairs with 256.  Same bits every way (tests compare
+ * them).  *previous (may be NULL) receives the old setting; other values
+ * BI_ERR_INVALID_ARG.
+ */
+BI_API bi_status bi_mx4_form(int32_t mode, int32_t *previous);
+
+/*
  * bi_fp32_fma_probe -- MEASUREMENT ONLY, not part of the MoE path: blocks x
  * 256 threads, each running 16 independent fp32 FMA chains for `iters`
  * steps (2 * 16 * iters flop per thread, no memory traffic in the loop).

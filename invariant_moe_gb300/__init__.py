@@ -41,6 +41,7 @@ EXPORTS = [
     "bi_ffn_workspace_bytes", "bi_ffn_forward", "bi_ffn_forward_train", "bi_ffn_backward",
     "bi_ffn_schedule",
     "bi_mx4_scale_bytes", "bi_mx4_quantize", "bi_mx4_dequantize", "bi_mx4_gemm", "bi_mx4_gate_up",
+    "bi_mx4_form",
 ]
 
 
@@ -111,6 +112,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             "bi_mx4_quantize": ([P, I32, I64, P, P, I64, I64, P], ST),
             "bi_mx4_dequantize": ([P, P, P, I32, I64, I64, I64, P], ST),
             "bi_mx4_gemm": ([P, P, P, P, P, I64, P, I64, I64, I64, I64, P], ST),
+            "bi_mx4_form": ([I32, P], ST),
             "bi_mx4_gate_up": ([P, P, P, P, P, I64, I64, I64, I64, P], ST),
             "bi_moe_scatter_contrib": ([P, P, P, P, I64, I64, I64, I32, P], ST),
         }
@@ -908,3 +910,11 @@ def bi_mx4_gate_up(xq, xs, w13q, w13s, out=None, stream=None):
     if st:
         _fail("bi_mx4_gate_up", st)
     return out
+
+
+def bi_mx4_form(mode):
+    """Which form of the kernel runs the 4-bit products (0 automatic, 1 single CTAs, 2 CTA pairs with 192 tokens
+    a tile, 3 CTA pairs with 256); returns the previous setting."""
+    prev = ctypes.c_int32(0)
+    _call("bi_mx4_form", int(mode), ctypes.byref(prev))
+    return prev.value

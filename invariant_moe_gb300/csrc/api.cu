@@ -1000,4 +1000,11 @@ BI_API bi_status bi_mx4_gate_up(const uint8_t *xq, const uint8_t *xs, const uint
   return mx4_product(xq, xs, w13q, w13s, nullptr, 0, act, ld_act, true, M, 2 * I, K, stream);
 }
 
+BI_API bi_status bi_mx4_form(int32_t mode, int32_t *previous) {
+  BI_REQUIRE(mode >= 0 && mode <= 3, BI_ERR_INVALID_ARG, "4-bit product form %d not in {0, 1, 2, 3}", mode);
+  const int old = bimoe::set_mx4_form(mode);
+  if (previous) *previous = old;
+  return BI_OK;
+}
+
 }  // extern "C"

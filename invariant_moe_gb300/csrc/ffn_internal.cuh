@@ -66,4 +66,6 @@ bi_status launch_mx4_dequantize(const uint8_t *q, const uint8_t *scales, void *y
 bi_status launch_mx4_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws, Mat addend,
                           __nv_bfloat16 *y, int64_t ldy, bool gated, int64_t M, int64_t N, int64_t K, cudaStream_t s);
 
+int set_mx4_form(int mode);  // bi_mx4_form; returns the old mode
+
 }  // namespace bimoe

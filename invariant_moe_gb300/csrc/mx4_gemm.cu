@@ -29,6 +29,7 @@
 // a tile of 192 tokens took 149 us for the first, a pair without the overlapping
 // accumulators' width (192 tokens) 89.6 (then 82.6 with it); blocks of 8 row tiles 84.9.  One token,
 // 4096 x 2048: 3.8 us, latency (4.5 MB are 0.7 us of copying).
+#include <atomic>
 #include <mutex>
 
 #include "tile_epilogue.cuh"
@@ -422,6 +423,11 @@ static bi_status launch_mx4(const CUtensorMap (&maps)[4], const Mx4Gemm &p, cuda
 
 static int div_up(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
+// 0: the form of least estimated time; 1 to 3: always that row of kForms.
+static std::atomic<int> g_mx4_form{0};
+
+int set_mx4_form(int mode) { return g_mx4_form.exchange(mode); }
+
 bi_status launch_mx4_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *wq, const uint8_t *ws, Mat addend,
                           __nv_bfloat16 *y, int64_t ldy, bool gated, int64_t M, int64_t N, int64_t K, cudaStream_t s) {
   Mx4Gemm p{};
@@ -445,10 +451,12 @@ bi_status launch_mx4_gemm(const uint8_t *xq, const uint8_t *xs, const uint8_t *w
     bool pair;
     int n, once, wave, stage;
   };
-  constexpr Form kForms[] = {{false, 128, 400, 100, 18}, {true, 192, 620, 70, 20}, {true, 256, 620, 60, 28}};
+  static constexpr Form kForms[] = {{false, 128, 400, 100, 18}, {true, 192, 620, 70, 20}, {true, 256, 620, 60, 28}};
+  const int form = g_mx4_form.load();
   int64_t best = INT64_MAX;
   bool pair = false;
   for (const Form &f : kForms) {
+    if (form != 0 && &f != &kForms[form - 1]) continue;
     const int64_t units = f.pair ? std::max(1, num_sms() / 2) : num_sms();
     const int64_t tiles = static_cast<int64_t>(div_up(N, f.pair ? 2 * kXRows : kXRows)) * div_up(M, f.n);
     const int64_t cost = f.once + (tiles + units - 1) / units * (f.wave + static_cast<int64_t>(f.stage) * p.nkb);
