@@ -337,3 +337,27 @@ def test_offsets_past_32_bits(cuda):
         assert torch.equal(o, out[s]) and torch.equal(g, gu[s]) and torch.equal(a, act[s])
         d = bm.bi_ffn_backward(dout[s], x[s], w13, w2, g, a, need=(True, False, False))[0]
         assert torch.equal(d, dx[s])
+
+
+PLANS = [
+    (129, 80, 48), (33, 80, 144),        # weight-gradient tiles of 128 columns, dx's tiles behind and before them
+    (129, 2064, 144), (70, 4112, 144),   # of 256 columns
+    (33, 80, 2064), (33, 272, 2064),     # dx by the split kernel, tiles of 128 and 256
+    (1025, 80, 48), (2100, 2064, 336)]   # more than one slice of tokens, 128 and 256
+
+
+@pytest.mark.parametrize("M,H,I", PLANS)
+def test_backward_by_every_plan(cuda, M, H, I):
+    """Every order and width that the backward's last launch chooses, bf16 and fp32 gradients."""
+    import invariant_moe_gb300 as bm
+    x, w13, w2, _, dout = make(M, H, I, 140)
+    r = ref.ffn(x, w13, w2, dout=dout)
+    b = ref.ffn_bounds(r, x, w13, w2, dout=dout)
+    args = [t.to(cuda) for t in (dout, x, w13, w2)]
+    _, gu, act = bm.bi_ffn_forward_train(*args[1:])
+    for name, t in zip(("dx", "dw13", "dw2"), bm.bi_ffn_backward(*args, gu, act)):
+        check(name, t, r, b, 2)
+    f13, f2 = torch.empty(2 * I, H, device=cuda), torch.empty(H, I, device=cuda)
+    _, f13, f2 = bm.bi_ffn_backward(*args, gu, act, dw13=f13, dw2=f2, need=(False, True, True))
+    check("dw13", f13, r, b, 1)
+    check("dw2", f2, r, b, 1)
