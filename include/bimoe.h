@@ -485,7 +485,8 @@ BI_API bi_status bi_moe_forward_noalloc(const bi_bf16 *x, const int32_t *ids,
  * Batch invariance: a row of out and of dx has the same bits whatever M is and
  * whatever other rows share the call (the reduction recipe is fixed by the
  * reduction length alone).  dW13 and dW2 sum over the tokens in a fixed
- * order: the same call gives the same bits.
+ * order, in slices of 1024 tokens added in fp32: the same call gives the same
+ * bits.
  * Requirements: H and I multiples of 16 and at most 2^20, M <= 2^30 (else
  * BI_ERR_UNSUPPORTED); pointers 16-byte aligned, the row strides ld* (in
  * elements) multiples of 8 and at least H.
@@ -721,7 +722,8 @@ BI_API bi_status bi_moe_decode_fused(int32_t mode, int32_t *previous);
 /*
  * bi_ffn_schedule -- which kernel runs the products of bi_ffn_forward,
  * bi_ffn_forward_train and bi_ffn_backward that have tokens as columns, for
- * the whole process from the next call on: 0 automatic (the default: by M),
+ * the whole process from the next call on: 0 automatic (the default: by M,
+ * the reductions' lengths and how many CTAs that gives),
  * 1 always the CTA-pair kernel, 2 the split kernel (the reduction's slices
  * over the CTAs of a cluster) wherever the reduction is at most 8192 long.
  * Same bits either way (tests compare them).  *previous (may be NULL) receives

@@ -1,7 +1,7 @@
 // api.cu -- the extern "C" entry points of libbimoe.so: argument checks,
 // workspace layout, TMA descriptor encoding, and the device error word.
-// All arithmetic happens in the kernels of router.cu, topk.cu, moe_route.cu,
-// moe_gemm.cu, ffn.cu and mx4.cu.
+// All arithmetic happens in the kernels of router.cu, router_topk.cu, topk.cu,
+// topk_window.cu, moe_route.cu, moe_gemm.cu, ffn.cu, mx4.cu and mx4_gemm.cu.
 #include <cstdarg>
 #include <cstdio>
 #include <atomic>

@@ -46,7 +46,9 @@ struct ContextSetup {
 // [box_rows, 64]-element box and 128-byte swizzle.  Returns false on failure.
 bool make_tma_2d_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                       uint32_t box_rows);
-// Same for a row-major fp32 tensor with a [box_rows, 32]-element box.
+// The same with row stride ld (elements).
+bool make_tma_2d_bf16_ld(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld,
+                         uint32_t box_rows);
 // The gate/up weights W13 [E, 2I, K] bf16 viewed as {K, 16, 2, E*2I/16}:
 // a box {64, 16, 2, 4} at group g lands 16 gate rows, the 16 up rows of the
 // same features (I rows further), and so on for four groups: 64 features'
@@ -54,28 +56,30 @@ bool make_tma_2d_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_
 // (`groups` 16-row gate/up pairs per copy, four unless said otherwise.)
 bool make_tma_inter_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t I, uint64_t K,
                          uint32_t groups = 4);
-// Encode a 2-D bf16 TMA map over [rows, cols] with row stride ld (elements) and
-// a [box_rows, 64]-element box, 128-byte swizzle.
-bool make_tma_2d_bf16_ld(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld,
-                         uint32_t box_rows);
-// Encode a 2-D byte map over a row-major [rows, row_bytes] array with a
-// [box_rows, 128]-byte box, 128-byte swizzle.
 // Encode a 2-D map over mx4 scale tiles [row_tiles][ktiles * 512 bytes] with a
 // box of two k tiles (1024 bytes) of box_rows row tiles, not swizzled.
 bool make_tma_mx_scales(CUtensorMap *map, const void *base, uint64_t row_tiles, uint64_t ktiles, uint32_t box_rows);
+// Encode a 2-D byte map over a row-major [rows, row_bytes] array with a
+// [box_rows, 128]-byte box, 128-byte swizzle.
 bool make_tma_2d_u8(CUtensorMap *map, const void *base, uint64_t rows, uint64_t row_bytes, uint32_t box_rows);
+// Encode a 2-D map over a row-major fp32 tensor with a [box_rows, 32]-element
+// box, 128-byte swizzle.
 bool make_tma_2d_f32(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                      uint32_t box_rows);
 void set_error(const char *fmt, ...);
 
 // Launches `kernel` as a programmatic dependent of the previous work on the
 // stream (programmatic stream serialization) and, for cluster_x > 1, in
-// clusters of cluster_x CTAs.  Every kernel of this library begins with
-// griddep_wait(), so its launch overlaps the end of its predecessor while
-// every memory access still follows it.  Only the short kernels with small
-// grids (griddep_wait_small_release) trigger their dependents early; for the
-// rest the trigger is each CTA's exit: CTAs of a dependent grid parked on the
-// SMs while a large grid runs were measured to slow it.
+// clusters of cluster_x CTAs.  Every kernel of this library waits for its
+// predecessor (griddep_wait) before it touches memory that another kernel may
+// write or read, so its launch overlaps the end of its predecessor.  One reads
+// before that: the feed-forward down kernel for few tokens loads W2, launched
+// behind its gate/up kernel, which writes no weights and triggers only after
+// its own wait.  Dependents are triggered early, always after that wait, by the
+// short kernels with small grids (griddep_wait_small_release), by the router's
+// rows schedule, by the feed-forward kernels but dact with wide tiles, and by the 4-bit product; for
+// the rest the trigger is each CTA's exit: CTAs of a dependent grid parked on
+// the SMs while a large grid runs were measured to slow it.
 template <typename... KArgs, typename... Args>
 bi_status launch_chained(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                          cudaStream_t stream, int cluster_x, Args... args) {

@@ -40,11 +40,14 @@
 // 1.70 held for seconds at the power cap):
 //   4096 tokens, H=4096, I=2048: forward 112 us, 1.84 PFLOP/s, with an addend 119
 //     (tensor cores; 4 waves of tiles of 224 tokens on 76 pairs);
-//   8191 tokens: forward 255 us, backward 550 us, 1.6 and 1.5 PFLOP/s (power: the
-//     SM clock falls to 1.5-1.6 GHz, where the tensor peak is 1.9);
-//   4096 tokens, H=2048, I=768: forward 36 us, backward 62 us (1.1 and 1.2
+//   8191 tokens: forward 238-256 us, backward 545 us, 1.6-1.7 and 1.5 PFLOP/s
+//     (power: the SM clock falls to 1.5-1.6 GHz, where the tensor peak is 1.9);
+//   4096 tokens, H=2048, I=768: forward 36 us, backward 63 us (1.1 and 1.2
 //     PFLOP/s: one to two waves of tiles, and the last tile's epilogue, 9 us in
 //     dact, which reads 8 bytes and writes 4 for each element);
+//   fp32 weight gradients instead of bf16 ones: 65.7 us for that backward, added
+//     to what is there 82.8 (a lane adds 32-byte pieces of its own row: the reads
+//     come late and apart);
 //   257 tokens, H=1040, I=720: step 29 us (six times a launch's fixed cost: set-up,
 //     first copies, the last tile).
 #include <atomic>
@@ -342,9 +345,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
   // The dependent grid may start: its CTAs need an SM of their own (this one's
   // shared memory is full), so they set up on SMs that are or become idle (a
   // training step of 257 tokens, H=1040, I=720: 32.8 -> 29.2 us).  Not behind
-  // dact with wide tiles, whose long epilogue got slower by as much again with
-  // CTAs parked beside it (4096 tokens, H=2048, I=768: step 98 us, with it 104;
-  // with tiles of 32 columns, 257 tokens, 30.2 without and 29.2 with it).
+  // dact with wide tiles, whose long epilogue gets slower with CTAs parked beside
+  // it.  The backward pass over six (H, I) from (1024, 512) to (4096, 2048),
+  // without and with the trigger: tiles of up to 64 columns (200 to 1000 tokens)
+  // 0.1 to 1.3 us less with it (H=1024, I=512, 200 tokens 13.7, 13.1); wider ones
+  // between 1.1 us less and 4 us more (H=1040, I=720, 2000 tokens 35.7, 34.6;
+  // H=2048, I=2048, 2000 tokens 80.3, 82.7; H=4096, I=2048, 3500 216, 220).
   if (EPI != kDact || one.n <= 64) griddep_launch_dependents();
 
   auto wait = [&](uint32_t bar, uint32_t parity, volatile int *ab) { return mbar_wait_cl(bar, parity, ab, batch.err); };
@@ -1040,9 +1046,12 @@ static bi_status launch_split(FfnGemm g, int64_t rows, int64_t M, int64_t K, boo
   p.g = g;
   p.err = device_error_word();
   const int slices = div_up(K, kSliceK), token_tiles = div_up(M, g.n);
-  // the tallest tiles that still give three CTAs to two SMs (H=4096, I=2048: 64
-  // rows a tile instead of 128 take 16.1 us instead of 18.7 for 32 tokens, 19.4
-  // instead of 22.9 for 64, the same for one), but not more than two to one
+  // the tallest tiles that still give three CTAs to two SMs, but not more than two
+  // to one.  Against tiles of 128 rows everywhere, the forward over seven (H, I)
+  // from (1024, 512) to (5120, 1408): one token 0 to 1.6 us less (H=4096, I=2048
+  // 15.7, 14.9), 16 tokens 1.8 to 3.1 (H=2048, I=2048 14.6, 11.5), 48 tokens 0 to
+  // 8.4 (22.3, 13.9), 96 tokens 0 to 7 (H=4096, I=1024 23.3, 16.3); as low as two
+  // to one allows them everywhere: level.
   p.tile_rows = kFM;
   const auto ctas = [&](int tile) { return static_cast<int64_t>(div_up(rows, tile)) * slices * token_tiles; };
   while (p.tile_rows > (A_MN ? 64 : 32) && ctas(p.tile_rows) * 2 < num_sms() * 3 &&

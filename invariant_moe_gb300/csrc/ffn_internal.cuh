@@ -7,11 +7,14 @@
 
 namespace bimoe {
 
-// 1 / (1 + exp(-g)) by the hardware's approximate exponential and reciprocal
-// (each within 2 ulp or so, far below the bf16 rounding that follows), with
-// subnormals flushed: as C++ intrinsics without flushing each takes several
-// instructions more, and the epilogues that need a sigmoid for every element
-// were bound by them.  For g below about -87 the result is 0, its limit.
+// 1 / (1 + exp(-g)) by the hardware's approximate exponential and reciprocal,
+// with subnormals flushed: as C++ intrinsics without flushing each takes
+// several instructions more, and the epilogues that need a sigmoid for every
+// element were bound by them.  Each is within 2 ulp or so of its argument's
+// value; the argument's own rounding, half an ulp of 1.44 |g|, makes the
+// exponential off by up to |g| 2^-24 more (5e-6 at g = -80), still far below
+// the bf16 rounding that follows.  For g below about -87 the result is 0, its
+// limit.
 __device__ __forceinline__ float sigmoid_approx(float g) {
   float e, s;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));

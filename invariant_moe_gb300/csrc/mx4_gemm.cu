@@ -26,9 +26,11 @@
 // 6.9 PFLOP/s, a tile some 9900 cycles of which 8190 are MMAs (the rest: handing the
 // accumulator over, about 1400, and waits for copies), 14 waves for 13.5; with
 // K = 8192 7.6 PFLOP/s.  Gated 4096 x 4096 x 4096: 25.0 us, 5.5 PFLOP/s.  One CTA
-// a tile of 192 tokens took 149 us for the first, a pair without the overlapping
-// accumulators' width (192 tokens) 89.6 (then 82.6 with it); blocks of 8 row tiles 84.9.  One token,
-// 4096 x 2048: 3.8 us, latency (4.5 MB are 0.7 us of copying).
+// a tile of 192 tokens took 149 us for the first, pairs of 192 tokens, whose
+// accumulators do not overlap, 89.6 (of 256 then 82.6; other sizes take 192, see
+// the launch); blocks of 8 row tiles 84.9.  One token, 4096 x 2048: 3.8 us, latency
+// (4.5 MB are 0.7 us of copying); gated 4096 x 4096 5.3 for one, 5.9 for 128.  An
+// addend costs more than its bytes: 8192 x 4096 x 2048 32.6 us, with one 70.8.
 #include <atomic>
 #include <mutex>
 
