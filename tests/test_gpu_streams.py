@@ -101,3 +101,26 @@ def test_results_dropped_on_the_current_stream(cuda):
     torch.cuda.synchronize()
     assert torch.equal(kept, want)
     del junk
+
+
+@pytest.mark.parametrize("name", ["forward", "backward", "four_bits", "layer"])
+def test_captured_on_a_forked_stream(cuda, name):
+    """Inside a graph capture, on a stream that is forked from the captured one and joined again."""
+    f = calls(cuda)[name]
+    want = [t.clone() for t in as_tuple(f(None))]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        first = as_tuple(f(side))
+        second = as_tuple(f(side))
+        torch.cuda.current_stream().wait_stream(side)
+        total = [a.float() + b.float() for a, b in zip(first, second)]
+    for _ in range(2):
+        for t in (*first, *second, *total):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for w, a, b, t in zip(want, first, second, total):
+            assert torch.equal(a, w) and torch.equal(b, w) and torch.equal(t, w.float() + w.float())
