@@ -261,8 +261,11 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 5)
   if (!beside) griddep_wait_small_release();
   const int e = blockIdx.x, h0 = blockIdx.y * kRouterCols, warp = threadIdx.x >> 5;
   const int beg = g.offsets[e], end = g.offsets[e + 1];
+  // beside: this grid is not done before dx' is, which later work takes for granted; with bad offsets neither
+  const bool last = beside && blockIdx.x == 0 && blockIdx.y == 0;
   if (beg < 0 || end < beg || end > g.P) {
     if (threadIdx.x == 0) report_error(err, BI_DEVERR_BAD_PERMUTATION);
+    if (last) griddep_wait();
     return;
   }
   const int col = (threadIdx.x & 31) * 8;
@@ -316,8 +319,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 5)
     for (int d = 16; d > 0; d >>= 1) bias = __fadd_rn(bias, __shfl_xor_sync(0xffffffffu, bias, d));
     if (threadIdx.x == 0) dbias[e] = add ? __fadd_rn(dbias[e], bias) : bias;
   }
-  // beside: this grid is not done before dx' is, which later work takes for granted
-  if (beside && blockIdx.x == 0 && blockIdx.y == 0) griddep_wait();
+  if (last) griddep_wait();
 }
 
 // ------------------------------------------------------------------- host --
