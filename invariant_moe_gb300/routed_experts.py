@@ -21,7 +21,8 @@ from .shared_expert import _rows16
 class _Gradients(torch.autograd.Function):
     """A backward pass as a node of its own: where a gradient is taken with create_graph=True its results stay
     connected to what they depend on (the tensors given besides the function), so that a second derivative, which
-    the library does not have, is refused instead of counted as zero."""
+    the library does not have, is refused instead of counted as zero.  (Those are the saved inputs of the forward
+    pass, so a copy that the library's layout needs is made outside of it, where autograd sees the copy.)"""
 
     @staticmethod
     def forward(ctx, f, *tensors):
@@ -47,7 +48,6 @@ def _plain(*tensors):
 class _GroupedLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, offsets):
-        x = _rows16(x)
         ctx.save_for_backward(x, w, offsets)
         return bi_grouped_gemm(x, w, offsets, out=x.new_zeros(x.shape[0], w.shape[1]))
 
@@ -66,8 +66,8 @@ class _GroupedLinear(torch.autograd.Function):
 def grouped_linear(x, w, offsets):
     """y [P,N] with y[p] = w[e] x[p] for offsets[e] <= p < offsets[e+1], rows of no group 0; x [P,K] and w [E,N,K]
     bf16, offsets int32 [E+1].  Differentiable in x and w."""
+    x = _rows16(x)
     if _plain(x, w):
-        x = _rows16(x)
         return bi_grouped_gemm(x, w, offsets, out=x.new_zeros(x.shape[0], w.shape[1]))
     return _GroupedLinear.apply(x, w, offsets)
 
@@ -79,7 +79,6 @@ def _unit_columns(t):
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
-        x = _unit_columns(x)
         y, mean, rstd = bi_layer_norm_train(x, weight, bias, eps)
         ctx.save_for_backward(x, weight, mean, rstd)
         ctx.param = next((t.dtype for t in (weight, bias) if t is not None), None)
@@ -100,16 +99,14 @@ class _LayerNorm(torch.autograd.Function):
 def layer_norm(x, weight=None, bias=None, eps=1e-5):
     """Layer norm over the last dimension of x [..., H] (bf16 or fp32), weight and bias [H] (bf16 or fp32) or None.
     Differentiable in x, weight and bias, whose gradients are summed in fp32."""
-    rows = x.reshape(-1, x.shape[-1])
-    y = bi_layer_norm(_unit_columns(rows), weight, bias, eps) if _plain(x, weight, bias) else _LayerNorm.apply(
-        rows, weight, bias, eps)
+    rows = _unit_columns(x.reshape(-1, x.shape[-1]))
+    y = (bi_layer_norm if _plain(x, weight, bias) else _LayerNorm.apply)(rows, weight, bias, eps)
     return y.view(x.shape)
 
 
 class _Experts(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, ids, wts, w13, w2):
-        x, wts = x.contiguous(), wts.contiguous()
         out, saved = bi_moe_forward_train(x, ids, wts, w13, w2)
         ctx.save_for_backward(ids, wts, w13, w2, x, *saved)
         ctx.saved_type = type(saved)
@@ -129,15 +126,15 @@ class _Experts(torch.autograd.Function):
 
 def routed_experts(x, ids, wts, w13, w2):
     """bi_moe_forward, differentiable in x [M,H], wts [M,k] (fp32), w13 [E,2I,H] and w2 [E,H,I]."""
+    x, wts = x.contiguous(), wts.contiguous()
     if _plain(x, wts, w13, w2):
-        return bi_moe_forward(x.contiguous(), ids, wts.contiguous(), w13, w2)
+        return bi_moe_forward(x, ids, wts, w13, w2)
     return _Experts.apply(x, ids, wts, w13, w2)
 
 
 class _MoeLayer(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_router, bias, w13, w2, top_k):
-        x = x.contiguous()
         scores, ids, wts, _ = bi_router_topk(x, w_router, top_k, bias=bias)
         out, saved = bi_moe_forward_train(x, ids, wts, w13, w2)
         ctx.save_for_backward(x, w_router, ids, wts, w13, w2, *saved)
@@ -165,8 +162,9 @@ class _MoeLayer(torch.autograd.Function):
 def moe_layer_train(x, w_router, w13, w2, top_k, bias=None):
     """moe_layer (the same bits up to H = 2048), differentiable in x, w_router, bias, w13 and w2.  Returns (out, scores, ids, wts);
     the last three carry no gradient."""
+    x = x.contiguous()
     if _plain(x, w_router, bias, w13, w2):
-        return bi_moe_layer(x.contiguous(), w_router, w13, w2, top_k, bias=bias)
+        return bi_moe_layer(x, w_router, w13, w2, top_k, bias=bias)
     return _MoeLayer.apply(x, w_router, bias, w13, w2, top_k)
 
 
