@@ -137,14 +137,14 @@ class _MoeLayer(torch.autograd.Function):
     def forward(ctx, x, w_router, bias, w13, w2, top_k):
         scores, ids, wts, _ = bi_router_topk(x, w_router, top_k, bias=bias)
         out, saved = bi_moe_forward_train(x, ids, wts, w13, w2)
-        ctx.save_for_backward(x, w_router, ids, wts, w13, w2, *saved)
+        ctx.save_for_backward(x, w_router, bias, ids, wts, w13, w2, *saved)
         ctx.saved_type = type(saved)
         ctx.mark_non_differentiable(scores, ids, wts)
         return out, scores, ids, wts
 
     @staticmethod
     def backward(ctx, dout, *unused):
-        x, w_router, ids, wts, w13, w2, *saved = ctx.saved_tensors
+        x, w_router, bias, ids, wts, w13, w2, *saved = ctx.saved_tensors
         saved, dout, n = ctx.saved_type(*saved), _rows16(dout).contiguous(), ctx.needs_input_grad
 
         def f():
@@ -156,7 +156,8 @@ class _MoeLayer(torch.autograd.Function):
                                                need=(False, n[1], n[2]))
             return dx, dw, db, dw13, dw2
 
-        return (*_gradients(f, dout, x, w_router, w13, w2), None)
+        # (everything depends on the bias through the routing weights)
+        return (*_gradients(f, dout, x, w_router, w13, w2, *(t for t in (bias,) if t is not None)), None)
 
 
 def moe_layer_train(x, w_router, w13, w2, top_k, bias=None):

@@ -92,7 +92,7 @@ FUNCTIONS = {
 # the functions whose gradient with respect to an argument depends on that argument, or may
 SECOND = [("layer_norm", "x"), ("layer_norm_weight", "x"), ("routed_experts", "x"), ("routed_experts", "wts"),
           ("routed_experts", "w13"), ("moe_layer_train", "x"), ("moe_layer_train", "router"),
-          ("moe_layer_train", "w13")]
+          ("moe_layer_train", "bias"), ("moe_layer_train", "w13")]
 
 
 def strided(t):
