@@ -47,7 +47,6 @@ class _FfnGradients(torch.autograd.Function):
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w13, w2, addend):
-        x, addend = _rows16(x), None if addend is None else _rows16(addend)
         out, gu, act = bi_ffn_forward_train(x, w13, w2, addend=addend)
         ctx.save_for_backward(x, w13, w2, gu, act)
         return out
@@ -64,11 +63,13 @@ class _GatedFfn(torch.autograd.Function):
 def gated_ffn(x, w13, w2, addend=None):
     """(silu(x Wg^T) * (x Wu^T)) W2^T (+ addend), differentiable once, in reverse mode, in every argument;
     x [M,H], w13 [2I,H], w2 [H,I] and addend [M,H] bf16."""
+    # (copies that the layout needs are made here, where autograd sees them)
+    x, addend = _rows16(x), None if addend is None else _rows16(addend)
     args = [t for t in (x, w13, w2, addend) if t is not None]
     # a tangent of forward-mode differentiation goes to the autograd function too, which refuses it
     if not (torch.is_grad_enabled() and any(t.requires_grad for t in args)) and all(
             unpack_dual(t).tangent is None for t in args):
-        return bi_ffn_forward(_rows16(x), w13, w2, addend=None if addend is None else _rows16(addend))
+        return bi_ffn_forward(x, w13, w2, addend=addend)
     return _GatedFfn.apply(x, w13, w2, addend)
 
 
