@@ -683,7 +683,8 @@ BI_API size_t bi_moe_train_workspace_bytes(int64_t M, int64_t H, int64_t E, int3
  *   gu     [P,2I] fp32 (16-byte aligned): g and u of each grouped row, for each
  *     16 features i.. the quads (g[i+j], g[i+j+8], u[i+j], u[i+j+8]), j = 0..7
  *   act    [P,I] bf16 (16-byte aligned)
- * Rows of x_perm, gu and act from offsets[E] on are left as they are.
+ * Rows of x_perm, gu and act from offsets[E] on are left as they are.  out may be
+ * x; what is written overlaps nothing else (BI_ERR_INVALID_ARG).
  */
 BI_API bi_status bi_moe_forward_train(const bi_bf16 *x, const int32_t *ids, const float *wts,
                                       const bi_bf16 *w13, const bi_bf16 *w2, bi_bf16 *out,
@@ -703,7 +704,9 @@ BI_API bi_status bi_moe_forward_train(const bi_bf16 *x, const int32_t *ids, cons
  *   dw13 [E,2I,H], dw2 [E,H,I] (16-byte aligned), or NULL each; grad_mode as
  *     bi_grouped_gemm_dw
  * dx may be dout or x.  M == 0: dw13 and dw2 are set to zero (grad_mode 2: left
- * as they are).
+ * as they are).  Otherwise dx and dwts overlap nothing that is given, dw13 and dw2
+ * none of offsets, x_perm and act, and the results not one another
+ * (BI_ERR_INVALID_ARG).
  */
 BI_API bi_status bi_moe_backward(const bi_bf16 *dout, const int32_t *ids, const float *wts,
                                  const bi_bf16 *w13, const bi_bf16 *w2, const int32_t *offsets,

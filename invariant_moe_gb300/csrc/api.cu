@@ -865,6 +865,31 @@ static bool overlap(const void *p, int64_t ldp, const void *q, int64_t ldq, int6
   return overlap_bytes(p, ldp * 2, cols * 2, q, ldq * 2, cols * 2, rows);
 }
 
+// An array of a call (p may be null: not given).
+struct Span {
+  const char *name;
+  const void *p;
+  int64_t bytes;
+};
+static bool spans_meet(const Span &a, const Span &b) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+  return p && q && p < q + static_cast<uintptr_t>(b.bytes) && q < p + static_cast<uintptr_t>(a.bytes);
+}
+// The results share no memory with one another nor with the operands; but `same` may be one of them, byte for byte,
+// for results[0].
+template <size_t R, size_t O>
+static bi_status check_apart(const Span (&results)[R], const Span (&operands)[O], const void *same = nullptr) {
+  for (size_t i = 0; i < R; ++i) {
+    for (size_t j = i + 1; j < R; ++j)
+      BI_REQUIRE(!spans_meet(results[i], results[j]), BI_ERR_INVALID_ARG, "%s and %s overlap", results[i].name,
+                 results[j].name);
+    for (const Span &o : operands)
+      BI_REQUIRE(!spans_meet(results[i], o) || (i == 0 && o.p == same && results[0].p == same), BI_ERR_INVALID_ARG,
+                 "%s overlaps %s", results[i].name, o.name);
+  }
+  return BI_OK;
+}
+
 static Mat mat(const bi_bf16 *p, int64_t ld) { return Mat{reinterpret_cast<const __nv_bfloat16 *>(p), ld}; }
 static const __nv_bfloat16 *cbf(const void *p) { return static_cast<const __nv_bfloat16 *>(p); }
 static __nv_bfloat16 *mbf(void *p) { return static_cast<__nv_bfloat16 *>(p); }
@@ -1158,10 +1183,16 @@ BI_API bi_status bi_moe_forward_train(const bi_bf16 *x, const int32_t *ids, cons
              BI_ERR_INVALID_ARG, "misaligned pointer (x/w13/w2/out/x_perm/gu/act 16 B, workspace 256 B)");
   const TrainWorkspace L = train_layout(M, H, E, top_k, I);
   BI_REQUIRE(workspace_bytes >= L.total, BI_ERR_WORKSPACE, "workspace %zu < %zu bytes", workspace_bytes, L.total);
+  const int64_t P = M * top_k;
+  const Span results[] = {{"out", out, M * H * 2},      {"offsets", offsets, (E + 1) * 4}, {"perm", perm, P * 4},
+                          {"slots", slots, M * 4},      {"x_perm", x_perm, P * H * 2},     {"gu", gu, P * 2 * I * 4},
+                          {"act", act, P * I * 2}};
+  const Span operands[] = {{"x", x, M * H * 2}, {"ids", ids, P * 4}, {"wts", wts, P * 4},
+                           {"w13", w13, E * 2 * I * H * 2}, {"w2", w2, E * H * I * 2}};
+  BI_TRY(check_apart(results, operands, x));
   char *ws = static_cast<char *>(workspace);
   float *contrib = reinterpret_cast<float *>(ws + L.contrib);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t P = M * top_k;
   const Groups g{offsets, static_cast<int>(E), static_cast<int>(P)};
   BI_TRY(launch_permute(ids, offsets, perm, M, E, top_k, ws + L.scratch, s, slots));
   // With one slot a token (the rows that an expert-parallel rank receives) nothing is summed: the down product's rows
@@ -1198,10 +1229,23 @@ BI_API bi_status bi_moe_backward(const bi_bf16 *dout, const int32_t *ids, const 
              BI_ERR_INVALID_ARG, "misaligned pointer (dout/w13/w2/x_perm/gu/act/w_router 16 B, workspace 256 B)");
   const TrainWorkspace L = train_layout(M, H, E, top_k, I);
   BI_REQUIRE(workspace_bytes >= L.total, BI_ERR_WORKSPACE, "workspace %zu < %zu bytes", workspace_bytes, L.total);
+  // dwts is set to zero first and dx may be; dw13 and dw2 come last, when only what is named here is still read
+  const int64_t P = M * top_k, grad = static_cast<int64_t>(grad_size(grad_mode));
+  const Span rows[] = {{"dx", dx, M * H * 2}, {"dwts", dwts, P * 4}};
+  const Span all[] = {{"dout", dout, M * H * 2},     {"ids", ids, P * 4},
+                      {"wts", wts, P * 4},           {"w13", w13, E * 2 * I * H * 2},
+                      {"w2", w2, E * H * I * 2},     {"offsets", offsets, (E + 1) * 4},
+                      {"perm", perm, P * 4},         {"slots", slots, M * 4},
+                      {"x_perm", x_perm, P * H * 2}, {"gu", gu, P * 2 * I * 4},
+                      {"act", act, P * I * 2},       {"w_router", w_router, E * H * 4}};
+  const Span weights[] = {{"dw13", dw13, E * 2 * I * H * grad}, {"dw2", dw2, E * H * I * grad}};
+  const Span late[] = {all[5], all[8], all[10], rows[0], rows[1]};
+  BI_TRY(check_apart(rows, all, dout));
+  BI_TRY(check_apart(weights, late));
   char *ws = static_cast<char *>(workspace);
   float *contrib = reinterpret_cast<float *>(ws + L.contrib), *parts = reinterpret_cast<float *>(ws + L.parts);
   __nv_bfloat16 *dout_perm = mbf(ws + L.dout), *dgu = mbf(ws + L.dgu);
-  const Groups g{offsets, static_cast<int>(E), static_cast<int>(M * top_k)};
+  const Groups g{offsets, static_cast<int>(E), static_cast<int>(P)};
   const bool through_router = dx && w_router;
   if (through_router && !dwts) dwts = reinterpret_cast<float *>(ws + L.dwts);
   const bool single = dx && top_k == 1 && !through_router;  // as in the forward pass

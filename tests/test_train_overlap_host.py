@@ -1,0 +1,87 @@
+"""Operators that train a routed-experts layer: results that would be written over what the call still reads are
+refused (no GPU: the addresses are never read)."""
+import ctypes
+
+import pytest
+
+NUL = ctypes.c_void_p(None)
+WS = ctypes.c_void_p(1 << 60)
+M, H, E, K, I = 8, 128, 4, 2, 128
+P = M * K
+BAD = 1
+
+
+def far(i):
+    return (i + 2) << 40
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from invariant_moe_gb300 import _build
+    _build.build()
+    import invariant_moe_gb300 as bm
+    return bm.load_library()
+
+
+# place among the arguments, bytes
+FORWARD = {"x": (0, M * H * 2), "ids": (1, P * 4), "wts": (2, P * 4), "w13": (3, E * 2 * I * H * 2),
+           "w2": (4, E * H * I * 2), "out": (5, M * H * 2), "offsets": (6, (E + 1) * 4), "perm": (7, P * 4),
+           "slots": (8, M * 4), "x_perm": (9, P * H * 2), "gu": (10, P * 2 * I * 4), "act": (11, P * I * 2)}
+BACKWARD = {"dout": (0, M * H * 2), "ids": (1, P * 4), "wts": (2, P * 4), "w13": (3, E * 2 * I * H * 2),
+            "w2": (4, E * H * I * 2), "offsets": (5, (E + 1) * 4), "perm": (6, P * 4), "slots": (7, M * 4),
+            "x_perm": (8, P * H * 2), "gu": (9, P * 2 * I * 4), "act": (10, P * I * 2), "w_router": (11, E * H * 4),
+            "dx": (12, M * H * 2), "dwts": (13, P * 4), "dw13": (14, E * 2 * I * H * 2), "dw2": (15, E * H * I * 2)}
+
+
+def places(table, over=None):
+    """The arguments, each far from the others; over: (name, other): name over other's first bytes, and over its
+    last 16."""
+    p = [far(i) for i in range(len(table))]
+    if over is None:
+        return [p]
+    name, other = over
+    out = []
+    for at in (p[table[other][0]], p[table[other][0]] + (table[other][1] - 16) // 16 * 16):
+        q = list(p)
+        q[table[name][0]] = at
+        out.append(q)
+    return out
+
+
+def forward(lib, p):
+    return lib.bi_moe_forward_train(*map(ctypes.c_void_p, p), M, H, E, K, I, WS, 1 << 40, NUL)
+
+
+def backward(lib, p):
+    return lib.bi_moe_backward(*map(ctypes.c_void_p, p), 0, M, H, E, K, I, WS, 1 << 40, NUL)
+
+
+@pytest.mark.parametrize("name", ["out", "offsets", "perm", "slots", "x_perm", "gu", "act"])
+def test_forward(lib, name):
+    for other in FORWARD:
+        if other == name or (name, other) == ("out", "x"):
+            continue
+        assert all(forward(lib, p) == BAD for p in places(FORWARD, (name, other))), other
+        assert name in lib.bi_last_error_message().decode() and "overlap" in lib.bi_last_error_message().decode()
+
+
+def test_forward_over_part_of_x(lib):
+    assert forward(lib, places(FORWARD, ("out", "x"))[1]) == BAD
+
+
+LATE = ("offsets", "x_perm", "act", "dx", "dwts")
+
+
+@pytest.mark.parametrize("name", ["dx", "dwts", "dw13", "dw2"])
+def test_backward(lib, name):
+    for other in BACKWARD:
+        if other == name or (name, other) == ("dx", "dout"):
+            continue
+        if name[:2] == "dw" and name != "dwts" and other not in LATE + ("dw13", "dw2"):
+            continue
+        assert all(backward(lib, p) == BAD for p in places(BACKWARD, (name, other))), other
+        assert name in lib.bi_last_error_message().decode() and "overlap" in lib.bi_last_error_message().decode()
+
+
+def test_backward_over_part_of_dout(lib):
+    assert backward(lib, places(BACKWARD, ("dx", "dout"))[1]) == BAD
