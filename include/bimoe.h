@@ -730,8 +730,9 @@ BI_API bi_status bi_moe_backward(const bi_bf16 *dout, const int32_t *ids, const 
  * A slot whose id is outside [0,E) or repeats an earlier slot of its row counts
  * for nothing.  A row of dx has the same bits in every batch.  Requirements:
  * H % 8 == 0, H <= 2^20, 1 <= E <= 1024, 1 <= top_k <= min(16, E),
- * M * top_k < 2^31; x, w, dx 16-byte aligned.  Where both dx and dw are
- * computed, dx must not overlap x nor dw overlap w (BI_ERR_INVALID_ARG).
+ * M * top_k < 2^31; x, w, dx 16-byte aligned.  dx, dw and dbias overlap nothing
+ * that the call reads, nor one another (BI_ERR_INVALID_ARG): dx may be x where dw
+ * is not computed, dw may be w where dx is not.
  */
 BI_API bi_status bi_router_backward(const float *dwts, const int32_t *ids, const float *wts,
                                     const void *x, int32_t x_f32, const float *w,

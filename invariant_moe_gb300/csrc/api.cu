@@ -1292,12 +1292,15 @@ BI_API bi_status bi_router_backward(const float *dwts, const int32_t *ids, const
              BI_ERR_INVALID_ARG, "null pointer");
   BI_REQUIRE(aligned(x, 16) && aligned(w, 16) && aligned(dx, 16), BI_ERR_INVALID_ARG,
              "x, w and dx must be 16-byte aligned");
-  // dw is summed while dx is stored
-  const int64_t dx_bytes = M * H * (x_f32 ? 4 : 2), w_bytes = E * H * 4;
-  BI_REQUIRE(!(dx && dw && overlap_bytes(dx, dx_bytes, dx_bytes, x, dx_bytes, dx_bytes, 1)), BI_ERR_INVALID_ARG,
-             "dx and x overlap");
-  BI_REQUIRE(!(dx && dw && overlap_bytes(dw, w_bytes, w_bytes, w, w_bytes, w_bytes, 1)), BI_ERR_INVALID_ARG,
-             "dw and w overlap");
+  // dw is summed while dx is stored; dx alone may be x, and dw alone w
+  const int64_t slots = M * top_k * 4, x_bytes = M * H * (x_f32 ? 4 : 2), w_bytes = E * H * 4;
+  const Span results[] = {{"dx", dx, x_bytes}, {"dw", dw, w_bytes}, {"dbias", dbias, E * 4}};
+  const Span operands[] = {{"dwts", dwts, slots},     {"ids", ids, slots},
+                           {"wts", wts, slots},       {"x", dw ? x : nullptr, x_bytes},
+                           {"w", dx ? w : nullptr, w_bytes},
+                           {"offsets", dw || dbias ? offsets : nullptr, (E + 1) * 4},
+                           {"perm", dw || dbias ? perm : nullptr, slots}};
+  BI_TRY(check_apart(results, operands));
   const GradCombine c{nullptr, nullptr, ids, wts, dwts, w, dx, x_f32 != 0, M, H, static_cast<int>(E), top_k,
                       dw || dbias};
   if (dx) BI_TRY(launch_grad_combine(c, nullptr, s));

@@ -85,3 +85,23 @@ def test_backward(lib, name):
 
 def test_backward_over_part_of_dout(lib):
     assert backward(lib, places(BACKWARD, ("dx", "dout"))[1]) == BAD
+
+
+# the router's gradient, of bf16 x; places among its arguments
+ROUTER = {"dwts": (0, P * 4), "ids": (1, P * 4), "wts": (2, P * 4), "x": (3, M * H * 2), "w": (5, E * H * 4),
+          "offsets": (6, (E + 1) * 4), "perm": (7, P * 4), "dx": (8, M * H * 2), "dw": (9, E * H * 4),
+          "dbias": (10, E * 4)}
+
+
+@pytest.mark.parametrize("name", ["dx", "dw", "dbias"])
+def test_router(lib, name):
+    for other, (at, size) in ROUTER.items():
+        if other == name:
+            continue
+        for start in (0, (size - 16) // 16 * 16):
+            p = [far(i) for i in range(11)]
+            p[4] = 0  # x is bf16
+            p[ROUTER[name][0]] = p[at] + start
+            assert lib.bi_router_backward(*[v if i == 4 else ctypes.c_void_p(v) for i, v in enumerate(p)], 0, M, H, E, K,
+                                          NUL) == BAD, other
+            assert "overlap" in lib.bi_last_error_message().decode()
