@@ -750,7 +750,8 @@ BI_API bi_status bi_router_backward(const float *dwts, const int32_t *ids, const
  *   mean, rstd [M] fp32, written, or NULL each: for bi_layer_norm_backward
  * A row of y has the same bits in every batch, at any stride and alignment.
  * Requirements: 1 <= H <= 16384, M <= 2^30, eps >= 0; pointers aligned to
- * their type.
+ * their type; y, mean and rstd overlap nothing else, nor one another
+ * (BI_ERR_INVALID_ARG).
  */
 BI_API bi_status bi_layer_norm(const void *x, int32_t x_f32, int64_t ldx, const void *weight,
                                const void *bias, int32_t p_f32, float eps, void *y, int64_t ldy,
@@ -765,6 +766,7 @@ BI_API bi_status bi_layer_norm(const void *x, int32_t x_f32, int64_t ldx, const 
  *   dy, x, dx have x's type; weight as in the forward; mean, rstd from it
  *   workspace: 16-byte aligned, bi_layer_norm_workspace_bytes(M, H) bytes, needed
  *     for dweight or dbias.
+ *   dx overlaps nothing else, and the results not one another (BI_ERR_INVALID_ARG)
  * A row of dx has the same bits in every batch; dweight and dbias add the rows in
  * an order that M and H fix.  M == 0: dweight and dbias are set to zero
  * (accumulate: left as they are).

@@ -1315,6 +1315,13 @@ static bi_status check_norm(int64_t M, int64_t H) {
              "unsupported norm (needs H <= 16384, M <= 2^30): M=%lld H=%lld", (long long)M, (long long)H);
   return BI_OK;
 }
+// An array against the `rows` rows of a matrix, `bytes` each, every ld bytes.
+static bool meets_rows(const Span &a, const void *m, int64_t ld, int64_t bytes, int64_t rows) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(m);
+  if (!p || !spans_meet(a, Span{"", m, (rows - 1) * ld + bytes})) return false;
+  const int64_t from = p > q ? static_cast<int64_t>(p - q) : 0, to = static_cast<int64_t>(p + a.bytes - q);
+  return from % ld < bytes || (from / ld + 1) * ld < to;  // in its row, or reaching into the next
+}
 static bi_status check_norm_rows(const char *name, const void *p, int64_t ld, int64_t H, int32_t f32) {
   BI_REQUIRE(p, BI_ERR_INVALID_ARG, "%s is NULL", name);
   BI_REQUIRE(aligned(p, f32 ? 4 : 2), BI_ERR_INVALID_ARG, "%s must be aligned to its type", name);
@@ -1336,6 +1343,13 @@ BI_API bi_status bi_layer_norm(const void *x, int32_t x_f32, int64_t ldx, const 
   const int64_t size = x_f32 ? 4 : 2;
   BI_REQUIRE((x == y && ldx == ldy) || !overlap_bytes(x, ldx * size, H * size, y, ldy * size, H * size, M),
              BI_ERR_INVALID_ARG, "x and y overlap (y may be x, with the same stride)");
+  const Span params[] = {{"weight", weight, H * (p_f32 ? 4 : 2)}, {"bias", bias, H * (p_f32 ? 4 : 2)}};
+  const Span stats[] = {{"mean", mean, M * 4}, {"rstd", rstd, M * 4}};
+  BI_TRY(check_apart(stats, params));
+  for (const Span &a : {params[0], params[1], stats[0], stats[1]})
+    BI_REQUIRE(!meets_rows(a, y, ldy * size, H * size, M), BI_ERR_INVALID_ARG, "y overlaps %s", a.name);
+  for (const Span &a : stats)
+    BI_REQUIRE(!meets_rows(a, x, ldx * size, H * size, M), BI_ERR_INVALID_ARG, "%s overlaps x", a.name);
   return launch_layer_norm(x, x_f32 != 0, ldx, weight, bias, p_f32 != 0, eps, y, ldy, mean, rstd, M, H,
                            reinterpret_cast<cudaStream_t>(stream));
 }
@@ -1370,7 +1384,13 @@ BI_API bi_status bi_layer_norm_backward(const void *dy, int64_t lddy, const void
     BI_REQUIRE(((dx == dy && lddx == lddy) || !overlap_bytes(dx, lddx * size, H * size, dy, lddy * size, H * size, M)) &&
                    ((dx == x && lddx == ldx) || !overlap_bytes(dx, lddx * size, H * size, x, ldx * size, H * size, M)),
                BI_ERR_INVALID_ARG, "dx overlaps dy or x (it may be either, with the same stride)");
+    for (const Span &a : {Span{"weight", weight, H * (p_f32 ? 4 : 2)}, Span{"mean", mean, M * 4},
+                          Span{"rstd", rstd, M * 4}, Span{"dweight", dweight, H * 4}, Span{"dbias", dbias, H * 4}})
+      BI_REQUIRE(!meets_rows(a, dx, lddx * size, H * size, M), BI_ERR_INVALID_ARG, "dx overlaps %s", a.name);
   }
+  // (dweight and dbias are written when everything has been read)
+  BI_REQUIRE(!spans_meet(Span{"dweight", dweight, H * 4}, Span{"dbias", dbias, H * 4}), BI_ERR_INVALID_ARG,
+             "dweight and dbias overlap");
   if (dweight || dbias) {
     const size_t need = layer_norm_workspace_bytes(M, H);
     BI_REQUIRE(workspace && aligned(workspace, 16), BI_ERR_INVALID_ARG, "workspace must be 16-byte aligned");

@@ -105,3 +105,49 @@ def test_router(lib, name):
             assert lib.bi_router_backward(*[v if i == 4 else ctypes.c_void_p(v) for i, v in enumerate(p)], 0, M, H, E, K,
                                           NUL) == BAD, other
             assert "overlap" in lib.bi_last_error_message().decode()
+
+
+# layer norm of 3 rows of 37 fp32 values, 48 apart: rows' bytes, then the vectors'
+ROWS, WIDTH, LD = 3, 37, 48
+
+
+def norm(lib, x, w, b, y, mean, rstd):
+    p = ctypes.c_void_p
+    return lib.bi_layer_norm(p(x), 1, LD, p(w), p(b), 1, ctypes.c_float(1e-5), p(y), LD, p(mean), p(rstd), ROWS, WIDTH,
+                             NUL)
+
+
+def norm_backward(lib, dx, w, mean, rstd, dw, db):
+    p = ctypes.c_void_p
+    return lib.bi_layer_norm_backward(p(far(20)), LD, p(far(21)), 1, LD, p(w), 1, p(mean), p(rstd), p(dx), LD, p(dw),
+                                      p(db), 0, ROWS, WIDTH, WS, 1 << 30, NUL)
+
+
+# a vector on a row's first and last value, across the start of the next row, and just before the rows
+def on_rows(base, size):
+    return [base, base + (LD + WIDTH - 1) * 4, base + (2 * LD) * 4 - 4 * (size > 4), base - 4 * (size > 4)]
+
+
+def test_norm(lib):
+    a = [far(i) for i in range(6)]  # x, w, b, y, mean, rstd
+
+    def call(**k):
+        v = dict(zip(("x", "w", "b", "y", "mean", "rstd"), a), **k)
+        return norm(lib, **v)
+
+    for rows, vectors in (("y", ("w", "b", "mean", "rstd")), ("x", ("mean", "rstd"))):
+        for v in vectors:
+            for at in on_rows(a["x w b y".split().index(rows)], 12):
+                assert call(**{v: at}) == BAD, (rows, v)
+                assert "overlap" in lib.bi_last_error_message().decode()
+    for v, o in (("mean", "rstd"), ("mean", "w"), ("rstd", "b")):
+        assert call(**{v: dict(zip(("w", "b", "rstd"), (a[1], a[2], a[5])))[o] + 8}) == BAD
+
+
+def test_norm_backward(lib):
+    a = {n: far(i) for i, n in enumerate(("dx", "w", "mean", "rstd", "dw", "db"))}
+    for v in ("w", "mean", "rstd", "dw", "db"):
+        for at in on_rows(a["dx"], 12):
+            assert norm_backward(lib, **dict(a, **{v: at})) == BAD, v
+            assert "dx overlaps" in lib.bi_last_error_message().decode()
+    assert norm_backward(lib, **dict(a, db=a["dw"] + 4)) == BAD
