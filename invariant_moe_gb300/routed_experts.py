@@ -9,12 +9,14 @@ differentiable once, in reverse mode; everything but autograd's bookkeeping runs
 in the library's kernels."""
 from __future__ import annotations
 
+import contextlib
+
 import torch
 from torch.autograd.forward_ad import unpack_dual
 
-from . import (bi_grouped_gemm, bi_grouped_gemm_dw, bi_grouped_gemm_dx, bi_layer_norm, bi_layer_norm_backward,
-               bi_layer_norm_train, bi_moe_backward, bi_moe_forward, bi_moe_forward_train, bi_moe_layer,
-               bi_router_backward, bi_router_topk)
+from . import (_current_device, bi_grouped_gemm, bi_grouped_gemm_dw, bi_grouped_gemm_dx, bi_layer_norm,
+               bi_layer_norm_backward, bi_layer_norm_train, bi_moe_backward, bi_moe_forward, bi_moe_forward_train,
+               bi_moe_layer, bi_router_backward, bi_router_topk)
 from .shared_expert import _rows16
 
 
@@ -43,6 +45,12 @@ def _plain(*tensors):
     tensors = [t for t in tensors if t is not None]
     return not (torch.is_grad_enabled() and any(t.requires_grad for t in tensors)) and all(
         unpack_dual(t).tangent is None for t in tensors)
+
+
+def _device_of(x):
+    """A context in which x's device is the current one, where the library's calls launch."""
+    at = x.get_device()
+    return torch.cuda.device(at) if at >= 0 and at != _current_device() else contextlib.nullcontext()
 
 
 class _GroupedLinear(torch.autograd.Function):
@@ -127,9 +135,8 @@ class _Experts(torch.autograd.Function):
 def routed_experts(x, ids, wts, w13, w2):
     """bi_moe_forward, differentiable in x [M,H], wts [M,k] (fp32), w13 [E,2I,H] and w2 [E,H,I]."""
     x, wts = x.contiguous(), wts.contiguous()
-    if _plain(x, wts, w13, w2):
-        return bi_moe_forward(x, ids, wts, w13, w2)
-    return _Experts.apply(x, ids, wts, w13, w2)
+    with _device_of(x):
+        return (bi_moe_forward if _plain(x, wts, w13, w2) else _Experts.apply)(x, ids, wts, w13, w2)
 
 
 class _MoeLayer(torch.autograd.Function):
@@ -164,9 +171,10 @@ def moe_layer_train(x, w_router, w13, w2, top_k, bias=None):
     """moe_layer (the same bits up to H = 2048), differentiable in x, w_router, bias, w13 and w2.  Returns (out, scores, ids, wts);
     the last three carry no gradient."""
     x = x.contiguous()
-    if _plain(x, w_router, bias, w13, w2):
-        return bi_moe_layer(x, w_router, w13, w2, top_k, bias=bias)
-    return _MoeLayer.apply(x, w_router, bias, w13, w2, top_k)
+    with _device_of(x):
+        if _plain(x, w_router, bias, w13, w2):
+            return bi_moe_layer(x, w_router, w13, w2, top_k, bias=bias)
+        return _MoeLayer.apply(x, w_router, bias, w13, w2, top_k)
 
 
 def moe_block(x, norm_weight, norm_bias, w_router, w13, w2, top_k, bias=None):

@@ -125,3 +125,35 @@ def test_gradients_of_strided_arguments(formulas, name):
         grads.append({n: t.grad for n, t in v.items() if t.grad is not None})
     assert grads[0] and grads[0].keys() == grads[1].keys()
     assert all(torch.equal(grads[0][n], grads[1][n]) for n in grads[0])
+
+
+@pytest.mark.parametrize("name", ["routed_experts", "moe_layer_train"])
+@pytest.mark.parametrize("grad", [False, True])
+def test_runs_with_the_tensors_device_current(formulas, monkeypatch, name, grad):
+    """Tensors of device 1 while device 0 is the current one: the calls underneath launch on the current device's
+    stream, so device 1 is made current around all of them."""
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            current.append(self.device)
+
+        def __exit__(self, *a):
+            current.pop()
+
+    for f in ("bi_moe_forward", "bi_moe_forward_train", "bi_moe_layer", "bi_router_topk"):
+        def call(*a, f=getattr(rx, f), **k):
+            seen.append(current[-1])
+            return f(*a, **k)
+        monkeypatch.setattr(rx, f, call)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(rx, "_current_device", lambda: current[-1], raising=False)
+    v = values(2)
+    if grad:
+        v["w2"].requires_grad_()
+    FUNCTIONS[name](v)
+    assert seen and set(seen) == {1} and current == [0]
