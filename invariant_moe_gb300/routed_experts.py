@@ -134,7 +134,7 @@ class _Experts(torch.autograd.Function):
 
 def routed_experts(x, ids, wts, w13, w2):
     """bi_moe_forward, differentiable in x [M,H], wts [M,k] (fp32), w13 [E,2I,H] and w2 [E,H,I]."""
-    x, wts = x.contiguous(), wts.contiguous()
+    x, wts = _rows16(x).contiguous(), wts.contiguous()
     with _device_of(x):
         return (bi_moe_forward if _plain(x, wts, w13, w2) else _Experts.apply)(x, ids, wts, w13, w2)
 
@@ -170,7 +170,7 @@ class _MoeLayer(torch.autograd.Function):
 def moe_layer_train(x, w_router, w13, w2, top_k, bias=None):
     """moe_layer (the same bits up to H = 2048), differentiable in x, w_router, bias, w13 and w2.  Returns (out, scores, ids, wts);
     the last three carry no gradient."""
-    x = x.contiguous()
+    x = _rows16(x).contiguous()
     with _device_of(x):
         if _plain(x, w_router, bias, w13, w2):
             return bi_moe_layer(x, w_router, w13, w2, top_k, bias=bias)

@@ -157,3 +157,31 @@ def test_runs_with_the_tensors_device_current(formulas, monkeypatch, name, grad)
         v["w2"].requires_grad_()
     FUNCTIONS[name](v)
     assert seen and set(seen) == {1} and current == [0]
+
+
+@pytest.mark.parametrize("name", ["routed_experts", "moe_layer_train"])
+@pytest.mark.parametrize("grad", [False, True])
+def test_rows_off_the_16_byte_grid(formulas, monkeypatch, name, grad):
+    """A contiguous x that starts off a 16-byte boundary is copied, not refused; and a copy is all that differs."""
+    def checked(f):
+        def call(x, *a, **k):
+            if x.data_ptr() % 16 or not x.is_contiguous():
+                raise RuntimeError("alignment")
+            return f(x, *a, **k)
+        return call
+
+    for f in ("bi_moe_forward", "bi_moe_forward_train", "bi_moe_layer"):
+        monkeypatch.setattr(rx, f, checked(getattr(rx, f)))
+    v = values(3)
+    want = FUNCTIONS[name](v)
+    flat = torch.empty(M * H + 16, dtype=BF)
+    at = (-flat.data_ptr() // 2) % 8 + 3
+    v["x"] = flat[at:at + M * H].view(M, H).copy_(v["x"]).detach().requires_grad_(grad)
+    assert v["x"].data_ptr() % 16 and v["x"].is_contiguous()
+    out = FUNCTIONS[name](v)
+    assert torch.equal(out, want)
+    if grad:
+        out.float().square().sum().backward()
+        got, v["x"] = v["x"].grad, v["x"].detach().clone().requires_grad_()
+        FUNCTIONS[name](v).float().square().sum().backward()
+        assert torch.equal(got, v["x"].grad)
