@@ -221,9 +221,12 @@ __global__ void __launch_bounds__(kStageThreads, 3) grad_combine_staged_kernel(G
 // A CTA of 8 warps per expert and 256 columns of x, 8 a lane: the warps take the
 // expert's positions in turn, kRouterUnroll rows under way at once, and their sums
 // are added in order.  The positions' (token, c) come into shared memory
-// kRouterBatch at a time.  Behind the kernel that stages W, `beside`: launched while
-// that one runs and waiting for it only at the end, as it reads nothing that one
-// writes (what came before is done when that one has begun).
+// kRouterBatch at a time, and the warps' sums are closed behind each batch, so that
+// no running sum of a long group is longer than 64 products or the number of its
+// batches (unclosed, 66048 equal products summed to 1.2e-4 too little).  Behind the
+// kernel that stages W, `beside`: launched while that one runs and waiting for it
+// only at the end, as it reads nothing that one writes (what came before is done
+// when that one has begun).
 // (4096 tokens, 256 experts, top 8, H=4096: 58 us, the rows of x from L2 top_k times
 // over at 4.6 TB/s; a warp's columns 512 or 1024 wide, so that (token, c) are made
 // fewer times: 74 and 111 us, held up by the largest group; columns of x in shared
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 5)
     router_dw_kernel(const float *__restrict__ dwts, const float *__restrict__ wts, const XT *__restrict__ x, Groups g,
                      const int32_t *__restrict__ perm, float *dw, float *dbias, int add, int H, int top_k, int beside,
                      int *err) {
-  __shared__ float s[kRouterWarps][kRouterCols];  // 8 KB
+  __shared__ __align__(16) float s[kRouterWarps][kRouterCols];  // 8 KB: each lane's sums of the batches so far
   __shared__ int token_s[kRouterBatch];
   __shared__ float c_s[kRouterBatch];
   if (!beside) griddep_wait_small_release();
@@ -271,7 +274,9 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 5)
   const int col = (threadIdx.x & 31) * 8;
   const bool in = dw && h0 + col < H;  // H is a multiple of 8
   const XT *from = x + h0 + col;
-  float acc[8] = {}, bias = 0.0f;
+  float4 *own = reinterpret_cast<float4 *>(&s[warp][col]);
+  own[0] = own[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float bias = 0.0f;
   for (int b0 = beg; b0 < end; b0 += kRouterBatch) {
     const int n = min(kRouterBatch, end - b0);
     for (int i = threadIdx.x; i < n; i += 32 * kRouterWarps) {
@@ -282,9 +287,13 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 5)
       c_s[i] = ok ? score_grad(dwts[pair], wts[pair]) : 0.0f;
     }
     __syncthreads();
-    if (threadIdx.x < 32 && dbias && h0 == 0)
-      for (int i = threadIdx.x; i < n; i += 32) bias = __fadd_rn(bias, c_s[i]);
+    if (threadIdx.x < 32 && dbias && h0 == 0) {
+      float part = 0.0f;
+      for (int i = threadIdx.x; i < n; i += 32) part = __fadd_rn(part, c_s[i]);
+      bias = __fadd_rn(bias, part);
+    }
     if (in) {
+      float acc[8] = {};
       for (int i0 = warp; i0 < n; i0 += kRouterWarps * kRouterUnroll) {
         // (loads without a condition and apart from their use, so that they are under way together: past the end
         // the last position's row again)
@@ -301,12 +310,16 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 5)
           for (int j = 0; j < 8; ++j) acc[j] = __fmaf_rn(c, v[u].at(j), acc[j]);
         }
       }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float4 t = own[j];
+        add4(t, make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]));
+        own[j] = t;
+      }
     }
     __syncthreads();
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) s[warp][col + j] = acc[j];
-  __syncthreads();
+  if (beg == end) __syncthreads();  // (the zeros of a group without positions)
   for (int i = threadIdx.x; i < kRouterCols && dw && h0 + i < H; i += 32 * kRouterWarps) {
     float t = 0.0f;
 #pragma unroll
