@@ -26,12 +26,17 @@
 //   * Recipe: the reduction in slices of 1024, each one chain of K=16 MMAs, the
 //     slices added in fp32 in increasing order by the epilogue warps while the next
 //     one runs (the tensor cores' additions truncate; slices bound what that costs
-//     over long reductions).  gate/up is one chain over H up to 2048, as in the
-//     inference kernel, whose bits it then has; beyond, slices: one chain leaves g
-//     and u 4.4e-6 too small at H=4096, which dwts, an fp32 result with all three
-//     factors' errors in it, would show as 1.3e-5 (with slices 6e-6; 32768 rows, 32
-//     groups, forward 1111 us, 1119).  dact is one chain over H: its epilogue is so
-//     long that it must not hold up the slices of the next tile (490 us, 400).
+//     over long reductions: a chain of n leaves its sum about 1.1e-9 n too small).
+//     gate/up is one chain over H up to 2048, as in the inference kernel, whose bits
+//     it then has; beyond, slices (32768 rows, 32 groups, H=4096, I=2048, forward:
+//     one chain 1111 us, slices 1119).  dact is cut into slices of 4096, as its long
+//     epilogue holds one of the two accumulators meanwhile and a shorter slice ends
+//     before it does (the same sizes, gather, dact and the parts' sum: slices of 4096
+//     478 us, of 2048 530, of 1024 567).  dwts, an fp32 result with the errors of g,
+//     u and dact in it, is 2.9e-6 too small in the 2-norm at H=1024, 6.4e-6 at 2048,
+//     6.3e-6 at 4096 and no more beyond (dact uncut: 2.1e-5 at 16384, 3.8e-5 at
+//     32768).  The down product of one slot a token is one chain over I, like the
+//     inference kernel's: it is rounded to bf16 at once.
 #include <mutex>
 
 #include "tile_epilogue.cuh"
@@ -53,11 +58,13 @@ constexpr int kTBarBytes = 512;
 constexpr int kTSmemMax = 227 * 1024;
 constexpr int kTSliceK = 1024;
 constexpr int kTOneChain = 2048;         // gate/up: one chain up to this H
+constexpr int kTDactSlice = 4096;        // dact: slices of this length
 static_assert((3 * kTMaxStages + 5) * 8 + 12 <= kTBarBytes, "barriers");
 
-// kGateUpLong: gate/up whose reduction has more than one slice.
-enum GroupedOp { kRows, kGateUp, kGateUpLong, kDact, kWgrad };
+// kGateUpLong, kDactLong: those whose reduction has more than one slice.
+enum GroupedOp { kRows, kGateUp, kGateUpLong, kDact, kDactLong, kWgrad };
 constexpr bool is_gate_up(GroupedOp op) { return op == kGateUp || op == kGateUpLong; }
+constexpr bool is_dact(GroupedOp op) { return op == kDact || op == kDactLong; }
 
 // Staging buffer of an epilogue warp (kWgrad: 32 rows x 128 bytes).
 __host__ __device__ constexpr int staging_bytes(GroupedOp op) { return op == kWgrad ? 4096 : kFStaging; }
@@ -83,10 +90,10 @@ struct GroupedArgs {
   int64_t ldo;
   int out_f32;         // kRows: fp32, else bf16
   int mode;            // kWgrad: a GradMode
-  const int32_t *perm; // kRows: rows go to row perm[p] (may be null: row p); kGateUp, kDact: index of wts
+  const int32_t *perm; // kRows: rows go to row perm[p] (may be null: row p); gate/up, dact: index of wts
   const float *wts;
-  float *gu;           // kGateUp: written; kDact: read
-  float *parts;        // kDact: sums over 32 features of dact silu(g) u, or null
+  float *gu;           // gate/up: written; dact: read
+  float *parts;        // dact: sums over 32 features of dact silu(g) u, or null
   int *err;
 };
 
@@ -672,7 +679,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
         if (bad) report_error(prm.err, BI_DEVERR_BAD_PERMUTATION);
       }
-      if (OP == kDact) {
+      if (is_dact(OP)) {
         // the projections that the epilogue reads, on their way to L2 while the tile is computed: 256 bytes for each
         // of the warp's columns
         const int row0 = ti.row + static_cast<int>(rank) * kTM + q * 32;
@@ -701,9 +708,9 @@ __global__ void __launch_bounds__(kTThreads, 1)
       const auto accumulator = [&] {
         return tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(buf * kTAccCols + h * ncols);
       };
-      if constexpr (is_gate_up(OP) || OP == kDact) {
+      if constexpr (is_gate_up(OP) || is_dact(OP)) {
         const uint32_t halves = 16u << 16;  // from a warp's first 16 lanes to the others
-        if constexpr (OP == kGateUpLong) {
+        if constexpr (OP == kGateUpLong || OP == kDactLong) {
           // the sums of all slices into the last one's accumulator
           float acc[8][2][8];
 #pragma unroll
@@ -955,7 +962,8 @@ bi_status launch_train_gate_up(const __nv_bfloat16 *x, Groups g, const int32_t *
 bi_status launch_train_dact(const __nv_bfloat16 *dout, Groups g, const int32_t *perm, const float *wts,
                             const __nv_bfloat16 *w2, const float *gu, __nv_bfloat16 *dgu, float *dw_parts, int64_t H,
                             int64_t I, cudaStream_t s) {
-  GroupedArgs p = problem(g, I, H, H, 2 * kTM, 2000);
+  const bool slices = H > kTDactSlice;
+  GroupedArgs p = problem(g, I, H, slices ? kTDactSlice : H, 2 * kTM, 2000);
   p.out = dgu;
   p.ldo = 2 * I;
   p.perm = perm;
@@ -963,7 +971,8 @@ bi_status launch_train_dact(const __nv_bfloat16 *dout, Groups g, const int32_t *
   p.gu = const_cast<float *>(gu);
   p.parts = dw_parts;
   p.early = 1;
-  return launch_over_rows<kDact, true>(p, Mat{dout, H}, w2, H, s);
+  return slices ? launch_over_rows<kDactLong, true>(p, Mat{dout, H}, w2, H, s)
+                : launch_over_rows<kDact, true>(p, Mat{dout, H}, w2, H, s);
 }
 
 bi_status launch_train_dx(const __nv_bfloat16 *dgu, Groups g, const int32_t *perm, const __nv_bfloat16 *w13, void *out,
