@@ -274,10 +274,23 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 5)
   const int col = (threadIdx.x & 31) * 8;
   const bool in = dw && h0 + col < H;  // H is a multiple of 8
   const XT *from = x + h0 + col;
+  float acc[8] = {}, bias = 0.0f;
+  // acc, this lane's sums of a batch, added to those of the batches before it
   float4 *own = reinterpret_cast<float4 *>(&s[warp][col]);
-  own[0] = own[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float bias = 0.0f;
+  const auto close = [&](bool first) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float4 t = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+      if (!first) add4(t, own[j]);
+      own[j] = t;
+    }
+  };
   for (int b0 = beg; b0 < end; b0 += kRouterBatch) {
+    if (b0 > beg) {
+      close(b0 == beg + kRouterBatch);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+    }
     const int n = min(kRouterBatch, end - b0);
     for (int i = threadIdx.x; i < n; i += 32 * kRouterWarps) {
       const int pair = perm[b0 + i];
@@ -293,7 +306,6 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 5)
       bias = __fadd_rn(bias, part);
     }
     if (in) {
-      float acc[8] = {};
       for (int i0 = warp; i0 < n; i0 += kRouterWarps * kRouterUnroll) {
         // (loads without a condition and apart from their use, so that they are under way together: past the end
         // the last position's row again)
@@ -310,16 +322,11 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 5)
           for (int j = 0; j < 8; ++j) acc[j] = __fmaf_rn(c, v[u].at(j), acc[j]);
         }
       }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float4 t = own[j];
-        add4(t, make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]));
-        own[j] = t;
-      }
     }
     __syncthreads();
   }
-  if (beg == end) __syncthreads();  // (the zeros of a group without positions)
+  close(end - beg <= kRouterBatch);
+  __syncthreads();
   for (int i = threadIdx.x; i < kRouterCols && dw && h0 + i < H; i += 32 * kRouterWarps) {
     float t = 0.0f;
 #pragma unroll
