@@ -683,8 +683,8 @@ BI_API size_t bi_moe_train_workspace_bytes(int64_t M, int64_t H, int64_t E, int3
  *   gu     [P,2I] fp32 (16-byte aligned): g and u of each grouped row, for each
  *     16 features i.. the quads (g[i+j], g[i+j+8], u[i+j], u[i+j+8]), j = 0..7
  *   act    [P,I] bf16 (16-byte aligned)
- * Rows of x_perm, gu and act from offsets[E] on are left as they are.  out may be
- * x; what is written overlaps nothing else (BI_ERR_INVALID_ARG).
+ * Rows of x_perm, gu and act from offsets[E] on are left as they are, and with
+ * M == 0 everything is.  out may be x; what is written overlaps nothing else (BI_ERR_INVALID_ARG).
  */
 BI_API bi_status bi_moe_forward_train(const bi_bf16 *x, const int32_t *ids, const float *wts,
                                       const bi_bf16 *w13, const bi_bf16 *w2, bi_bf16 *out,

@@ -1153,7 +1153,7 @@ static TrainWorkspace train_layout(int64_t M, int64_t H, int64_t E, int32_t top_
     off += align256(bytes);
     return at;
   };
-  w.contrib = take(P * H * sizeof(float));
+  w.contrib = take(P * H * sizeof(float));  // (one slot a token: for dx through the router only, which no size says)
   w.scratch = off;  // the forward's permutation; the backward's buffers take the same place
   const size_t scratch = align256(permute_scratch_bytes(M, E));
   w.dout = take(P * H * 2);

@@ -77,14 +77,26 @@ void set_error(const char *fmt, ...);
 // stream (programmatic stream serialization) and, for cluster_x > 1, in
 // clusters of cluster_x CTAs.  Every kernel of this library waits for its
 // predecessor (griddep_wait) before it touches memory that another kernel may
-// write or read, so its launch overlaps the end of its predecessor.  One reads
-// before that: the feed-forward down kernel for few tokens loads W2, launched
-// behind its gate/up kernel, which writes no weights and triggers only after
-// its own wait.  Dependents are triggered early, always after that wait, by the
-// short kernels with small grids (griddep_wait_small_release), by the router's
-// rows schedule, by the feed-forward kernels but dact with wide tiles, and by the 4-bit product; for
-// the rest the trigger is each CTA's exit: CTAs of a dependent grid parked on
-// the SMs while a large grid runs were measured to slow it.
+// write or read, so its launch overlaps the end of its predecessor.  Three read
+// before that what the kernel in front of them, always one of the same call, does
+// not write; that one triggers only after its own wait, so whatever came before
+// it is complete:
+//   * the feed-forward down kernel for few tokens: W2 (behind its gate/up kernel);
+//   * grouped_kernel with `early` (the training step's gate/up, dact, dx and, with
+//     one slot a token, down): offsets and the weights (behind a gather, dact, the
+//     sum of dwts' parts or gate/up);
+//   * router_dw_kernel with `beside`: all its inputs (behind the staged dx kernel,
+//     which writes dx alone, and dx overlaps none of them).  It waits at its end, so
+//     that whoever waits for it has dx too.
+// Nothing is written before the wait but by the last of these, which writes dw and
+// dbias: these overlap nothing that the staged dx kernel reads.
+// Dependents are triggered early, always after that wait, by the short kernels
+// with small grids (griddep_wait_small_release), by the router's rows schedule, by
+// the feed-forward kernels but dact with wide tiles, by the 4-bit product, by
+// grouped_kernel and the staged dx kernel (at their start) and by the norm's
+// backward kernel (behind its rows); for the rest the trigger is each CTA's exit:
+// CTAs of a dependent grid parked on the SMs while a large grid runs were measured
+// to slow it.
 template <typename... KArgs, typename... Args>
 bi_status launch_chained(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                          cudaStream_t stream, int cluster_x, Args... args) {

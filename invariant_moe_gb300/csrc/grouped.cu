@@ -97,7 +97,9 @@ struct GroupedArgs {
   int *err;
 };
 
-// The two projections' gradients and the weight's from dact = d: one fixed fp32 sequence.
+// The two projections' gradients and the weight's from dact = d: one fixed fp32 sequence.  (Its sigmoid is not
+// the one of swiglu_p_f32, which has the inference kernel's bits: both are within a few units of the last place, far
+// below the bf16 rounding of act, dg and du.)
 struct GateGradsW {
   float dg, du, dw;
 };
@@ -197,8 +199,8 @@ __device__ __forceinline__ void rows_epilogue(const GroupedArgs &p, const float 
 
 // Epilogues of one warp of gate/up and of dact, from tensor memory at t: a chunk of
 // 16 columns at a time in a loop that is not unrolled (eight chunks' code behind
-// one another did not fit the instruction cache: dact of 32768 rows, 32 groups,
-// H=4096, I=2048 490 us, so 400).
+// one another does not fit the instruction cache: gather, dact and the parts' sum
+// of 32768 rows, 32 groups, H=4096, I=2048 516 us, so 478).
 __device__ __forceinline__ void chunk_weights(const ColumnInfo &col, int c, int lane, float (&w)[4]) {
   const float v = c < 2 ? col.w[0] : c < 4 ? col.w[1] : c < 6 ? col.w[2] : col.w[3];
 #pragma unroll

@@ -227,8 +227,9 @@ __global__ void __launch_bounds__(kStageThreads, 3) grad_combine_staged_kernel(G
 // kernel that stages W, `beside`: launched while that one runs and waiting for it
 // only at the end, as it reads nothing that one writes (what came before is done
 // when that one has begun).
-// (4096 tokens, 256 experts, top 8, H=4096: 58 us, the rows of x from L2 top_k times
-// over at 4.6 TB/s; a warp's columns 512 or 1024 wide, so that (token, c) are made
+// (4096 tokens, 256 experts, top 8, H=4096, with L2 emptied before: 50 us with groups
+// of up to 1018 positions, 40 with even ones, the rows of x from L2 top_k times over,
+// 268 MB.  Measured beside 58 with warm inputs and uneven groups: a warp's columns 512 or 1024 wide, so that (token, c) are made
 // fewer times: 74 and 111 us, held up by the largest group; columns of x in shared
 // memory, read once: 181 us, the latencies of a warp's experts one after another.)
 constexpr int kRouterBatch = 512, kRouterUnroll = 4, kRouterWarps = 8, kRouterCols = 256;

@@ -5,8 +5,13 @@ and router as differentiable functions.
 ``layer_norm`` the norm before a layer, ``routed_experts`` the gated experts under
 a given routing, ``moe_layer_train`` the whole layer (router, top-k, experts) and
 ``moe_block`` the layer behind its norm, added to its input.  Each is
-differentiable once, in reverse mode; everything but autograd's bookkeeping runs
-in the library's kernels."""
+differentiable once, in reverse mode; their products, sums and norms run in the
+library's kernels, copies of inputs that lie off its layout, grouped_linear's rows
+of no group and moe_block's sum in torch's.
+
+A backward pass is captured into a CUDA graph only while no eager graph of the same
+leaves is alive: such a graph keeps the stream on which autograd adds up a leaf's
+gradient, and a capture cannot wait for another stream's work."""
 from __future__ import annotations
 
 import contextlib
